@@ -8,6 +8,9 @@ call fails, an exception is raised.
 
     out, hT = kda_chunk_fwd(q, k, v, g, beta, h0=None, cu_seqlens=None)
     out     = kda_decode_step(q, k, v, g, beta, S)        # S updated in place
+    kda_latent_append(kv, kv_cache, page_table, seq_lens, rank=512, ...)
+    out, lse = kda_latent_attn(q, kv_cache, page_table, seq_lens, rank=512, scale=s)
+    tokens, accepted = kda_verify_tokens(target, draft, draft_tokens, uniforms)
     grads   = kda_chunk_bwd(q, k, v, g, beta, dout, h0=None, dhT=None, cu_seqlens=None)
 """
 from __future__ import annotations
@@ -25,7 +28,8 @@ __all__ = ["kda_chunk_fwd", "kda_chunk_fwd_fused", "kda_chunk_bwd", "kda_device_
            "lib", "library_path", "header_symbols", "KdaError",
            "KDA_OK", "KDA_ERR_INVALID_ARG", "KDA_ERR_UNSUPPORTED", "KDA_ERR_CUDA",
            "KDA_ERR_TIMEOUT", "KDA_BF16", "KDA_F32", "KDA_OP_CHUNK_FWD", "KDA_OP_CHUNK_BWD",
-           "kda_workspace_size", "kda_pool_usage"]
+           "kda_workspace_size", "kda_pool_usage", "kda_latent_append", "kda_latent_attn",
+           "kda_latent_attn_workspace_size", "kda_verify_tokens"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _ROOT = os.path.dirname(_PKG)
@@ -118,6 +122,17 @@ def lib() -> ctypes.CDLL:
         L.kda_chunk_bwd_ws.argtypes = [vp, vp, vp, fp, fp, fp, vp, vp, fp,
                                        fp, fp, fp, fp, fp, fp] + [ip] * 7 + [vp, sz, vp]
         L.kda_chunk_bwd_ws.restype = ctypes.c_int
+        ll, cf = ctypes.c_longlong, ctypes.c_float
+        L.kda_latent_append.argtypes = [vp] * 9 + [ip] * 8 + [ll] * 7 + [cf, ip, ip, vp]
+        L.kda_latent_append.restype = ctypes.c_int
+        L.kda_latent_attn.argtypes = [vp] * 7 + [ip] * 8 + [ll, ll, cf, ip, vp]
+        L.kda_latent_attn.restype = ctypes.c_int
+        L.kda_latent_attn_ws.argtypes = L.kda_latent_attn.argtypes[:-1] + [vp, sz, vp]
+        L.kda_latent_attn_ws.restype = ctypes.c_int
+        L.kda_latent_attn_workspace_size.argtypes = [ip] * 9 + [ctypes.POINTER(sz)]
+        L.kda_latent_attn_workspace_size.restype = ctypes.c_int
+        L.kda_verify_tokens.argtypes = [vp] * 7 + [ip] * 3 + [vp]
+        L.kda_verify_tokens.restype = ctypes.c_int
         L.kda_pool_usage.argtypes = [ip, ctypes.POINTER(ctypes.c_ulonglong)]
         L.kda_pool_usage.restype = ctypes.c_int
         _lib = L
@@ -201,7 +216,8 @@ def kda_prefill_plan(B: int, T: int, H: int, packed: bool = False, sms: int = 14
 
 
 KERNEL_KINDS = {"prep": 0, "state": 1, "combine": 2, "fused": 3, "simt": 4, "decode": 5,
-                "bwd": 6, "bwd_prep": 7, "bwd_chain": 8, "bwd_grad": 9}
+                "bwd": 6, "bwd_prep": 7, "bwd_chain": 8, "bwd_grad": 9, "latent_append": 10,
+                "latent_attn": 11, "verify": 12}
 
 
 def kda_timing_start() -> None:
@@ -538,3 +554,200 @@ def kda_decode_chunk(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch
     if rc != KDA_OK:
         raise KdaError("kda_decode_chunk", rc)
     return out
+
+
+# ------------------------------------------------ latent attention, drafted tokens
+
+def _run_on(device: torch.device, stream, call, fn: str) -> None:
+    """call(stream handle) with `device` current (the library works on the current one)."""
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            rc = call(_stream(stream))
+    else:
+        rc = call(_stream(stream))
+    if rc != KDA_OK:
+        raise KdaError(fn, rc)
+
+
+def _same_device(device: torch.device, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _latent_args(B: int, T: int, D: int, dtype, kv_cache: torch.Tensor, page_table: torch.Tensor,
+                 seq_lens: torch.Tensor, cu_seqlens: Optional[torch.Tensor], rank: int):
+    """Checks shared by kda_latent_append and kda_latent_attn; (dtype id, sequences, rope)."""
+    dt = _DTYPES.get(dtype)
+    if dt is None:
+        raise ValueError(f"unsupported dtype {dtype}")
+    if kv_cache.dim() != 3 or kv_cache.shape[2] != D or kv_cache.dtype != dtype:
+        raise ValueError(f"kv_cache must be [pages, page_size, {D}] of {dtype}, got "
+                         f"{tuple(kv_cache.shape)} of {kv_cache.dtype}")
+    if not kv_cache.is_cuda or kv_cache.stride(2) != 1:
+        raise ValueError("kv_cache must be a CUDA tensor with contiguous rows")
+    _check("seq_lens", seq_lens, torch.int32)
+    nseq = seq_lens.numel()
+    if cu_seqlens is not None:
+        _check("cu_seqlens", cu_seqlens, torch.int32, (nseq + 1,))
+        if B != 1:
+            raise ValueError("packed inputs (cu_seqlens) must have B == 1")
+    elif nseq != B:
+        raise ValueError(f"seq_lens has {nseq} entries for {B} sequences")
+    _check("page_table", page_table, torch.int32)
+    if page_table.dim() != 2 or page_table.shape[0] != nseq:
+        raise ValueError(f"page_table must be [{nseq}, max_pages], got {tuple(page_table.shape)}")
+    if not 0 < rank <= D:
+        raise ValueError(f"rank {rank} does not fit rows of {D}")
+    return dt, nseq, D - rank
+
+
+def _token_stride(name: str, t: torch.Tensor) -> int:
+    """Elements from one token of t [B, T, ..] to the next, which has to hold across B."""
+    if t.shape[0] > 1 and t.shape[1] > 1 and t.stride(0) != t.shape[1] * t.stride(1):
+        raise ValueError(f"{name}'s sequences must follow each other at its token stride")
+    return t.stride(1) if t.shape[1] > 1 else t.stride(0) if t.shape[0] > 1 else 0
+
+
+def kda_latent_append(kv: torch.Tensor, kv_cache: torch.Tensor, page_table: torch.Tensor,
+                      seq_lens: torch.Tensor, *, rank: int,
+                      cu_seqlens: Optional[torch.Tensor] = None,
+                      norm_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                      inv_freq: Optional[torch.Tensor] = None, interleaved: bool = False,
+                      q_pe: Optional[torch.Tensor] = None,
+                      q_pe_out: Optional[torch.Tensor] = None, stream=None):
+    """Norm, rotate and write the new tokens' latent rows to the paged cache, in place.
+    kv [N, L, rank + rope] (or [1, T, ..] with cu_seqlens int32 [N+1]); kv_cache
+    [pages, page_size, rank + rope]; page_table int32 [N, max_pages]; seq_lens int32 [N],
+    lengths with the new tokens; norm_weight f32 [rank] or None; inv_freq f32 [rope/2] or
+    None.  With q_pe [N, L, H, rope], its rotation goes to q_pe_out (default: a new
+    tensor), e.g. the view q[..., rank:] of the queries kda_latent_attn takes.  kv, q_pe
+    and q_pe_out may be strided over tokens and heads.  Returns q_pe_out (None without)."""
+    if kv.dim() != 3:
+        raise ValueError("kv must be [B, T, rank + rope]")
+    B, T, D = kv.shape
+    dt, nseq, rope = _latent_args(B, T, D, kv.dtype, kv_cache, page_table, seq_lens, cu_seqlens,
+                                  rank)
+    if not kv.is_cuda or kv.stride(2) != 1:
+        raise ValueError("kv must be a CUDA tensor with contiguous rows")
+    if norm_weight is not None:
+        _check("norm_weight", norm_weight, torch.float32, (rank,))
+    if inv_freq is not None:
+        _check("inv_freq", inv_freq, torch.float32, (rope // 2,))
+    H, qs = 1, [0, 0, 0, 0]
+    if q_pe is None and q_pe_out is not None:
+        raise ValueError("q_pe_out needs q_pe")
+    if q_pe is not None:
+        if q_pe_out is None:
+            q_pe_out = torch.empty(q_pe.shape, dtype=q_pe.dtype, device=q_pe.device)
+        H = q_pe.shape[2] if q_pe.dim() == 4 else 0
+        for i, (name, t) in enumerate((("q_pe", q_pe), ("q_pe_out", q_pe_out))):
+            if t.dim() != 4 or tuple(t.shape) != (B, T, H, rope) or t.dtype != kv.dtype:
+                raise ValueError(f"{name} must be [{B}, {T}, H, {rope}] of {kv.dtype}, got "
+                                 f"{tuple(t.shape)} of {t.dtype}")
+            if not t.is_cuda or t.stride(3) != 1:
+                raise ValueError(f"{name} must be a CUDA tensor with contiguous rows")
+            qs[2 * i] = _token_stride(name, t) or H * rope
+            qs[2 * i + 1] = t.stride(2) if H > 1 else rope
+    _same_device(kv.device, kv_cache=kv_cache, page_table=page_table, seq_lens=seq_lens,
+                 cu_seqlens=cu_seqlens, norm_weight=norm_weight, inv_freq=inv_freq, q_pe=q_pe,
+                 q_pe_out=q_pe_out)
+    L_ = lib()
+    _run_on(kv.device, stream, lambda st: L_.kda_latent_append(
+        _ptr(kv), _ptr(norm_weight), _ptr(inv_freq), _ptr(q_pe), _ptr(q_pe_out), _ptr(kv_cache),
+        _ptr(page_table), _ptr(seq_lens), _ptr(cu_seqlens), nseq, T, H, rank, rope,
+        kv_cache.shape[0], kv_cache.shape[1], page_table.shape[1], kv_cache.stride(0),
+        kv_cache.stride(1), _token_stride("kv", kv) or D, *qs, eps, int(interleaved), dt, st),
+        "kda_latent_append")
+    return q_pe_out
+
+
+def kda_latent_attn_workspace_size(N: int, L: int, H: int, rank: int, rope: int, page_size: int,
+                                   packed: bool = False, dtype: int = KDA_BF16,
+                                   sms: int = 0) -> int:
+    """Workspace bytes of one kda_latent_attn call (L: new tokens a sequence, packed: in
+    all); sms = 0 asks the current device."""
+    out = ctypes.c_size_t(0)
+    rc = lib().kda_latent_attn_workspace_size(N, L, H, rank, rope, page_size, int(bool(packed)),
+                                              int(dtype), int(sms), ctypes.byref(out))
+    if rc != KDA_OK:
+        raise KdaError("kda_latent_attn_workspace_size", rc)
+    return int(out.value)
+
+
+def kda_latent_attn(q: torch.Tensor, kv_cache: torch.Tensor, page_table: torch.Tensor,
+                    seq_lens: torch.Tensor, *, rank: int, scale: float,
+                    cu_seqlens: Optional[torch.Tensor] = None,
+                    out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None, stream=None):
+    """Absorbed latent attention of the new tokens over the paged cache, causal.
+    q [N, L, H, rank + rope] (or [1, T, H, ..] with cu_seqlens int32 [N+1]); kv_cache
+    [pages, page_size, rank + rope]; page_table int32 [N, max_pages]; seq_lens int32 [N],
+    lengths with the new tokens.  Returns (out [.., H, rank] in q's type, lse [.., H] f32,
+    the natural log of the scores' summed exponentials); a token that sees nothing gives 0
+    and -inf.  A ``workspace`` tensor (kda_latent_attn_workspace_size bytes) calls
+    kda_latent_attn_ws on it."""
+    if q.dim() != 4:
+        raise ValueError("q must be [B, T, H, rank + rope]")
+    B, T, H, D = q.shape
+    _check("q", q)
+    dt, nseq, rope = _latent_args(B, T, D, q.dtype, kv_cache, page_table, seq_lens, cu_seqlens,
+                                  rank)
+    if out is None:
+        out = torch.empty((B, T, H, rank), dtype=q.dtype, device=q.device)
+    else:
+        _check("out", out, q.dtype, (B, T, H, rank))
+    if lse is None:
+        lse = torch.empty((B, T, H), dtype=torch.float32, device=q.device)
+    else:
+        _check("lse", lse, torch.float32, (B, T, H))
+    _same_device(q.device, kv_cache=kv_cache, page_table=page_table, seq_lens=seq_lens,
+                 cu_seqlens=cu_seqlens, out=out, lse=lse, workspace=workspace)
+    args = [_ptr(q), _ptr(kv_cache), _ptr(page_table), _ptr(seq_lens), _ptr(cu_seqlens), _ptr(out),
+            _ptr(lse), nseq, T, H, rank, rope, kv_cache.shape[0], kv_cache.shape[1],
+            page_table.shape[1], kv_cache.stride(0), kv_cache.stride(1), scale, dt]
+    L_ = lib()
+    if workspace is not None:
+        args += _workspace_args(workspace)
+        _run_on(q.device, stream, lambda st: L_.kda_latent_attn_ws(*args, st), "kda_latent_attn_ws")
+    else:
+        _run_on(q.device, stream, lambda st: L_.kda_latent_attn(*args, st), "kda_latent_attn")
+    return out, lse
+
+
+def kda_verify_tokens(target: torch.Tensor, draft: Optional[torch.Tensor],
+                      draft_tokens: torch.Tensor, uniforms: torch.Tensor,
+                      draft_lens: Optional[torch.Tensor] = None,
+                      tokens: Optional[torch.Tensor] = None,
+                      accepted: Optional[torch.Tensor] = None, stream=None):
+    """Which drafted tokens stand, and the token after them.  target [N, L+1, V] f32;
+    draft [N, L, V] f32, or None where each drafted token was certain; draft_tokens int32
+    [N, L]; uniforms f32 [N, L+1] in [0, 1) (the last draws the token after the accepted
+    ones); draft_lens int32 [N] or None (L each).  Returns (tokens int32 [N, L+1]: the
+    accepted drafts, the drawn token, then -1; accepted int32 [N])."""
+    if target.dim() != 3:
+        raise ValueError("target must be [N, L + 1, V]")
+    N, L1, V = target.shape
+    L = L1 - 1
+    _check("target", target, torch.float32)
+    if draft is not None:
+        _check("draft", draft, torch.float32, (N, L, V))
+    _check("draft_tokens", draft_tokens, torch.int32, (N, L))
+    _check("uniforms", uniforms, torch.float32, (N, L1))
+    if draft_lens is not None:
+        _check("draft_lens", draft_lens, torch.int32, (N,))
+    if tokens is None:
+        tokens = torch.empty((N, L1), dtype=torch.int32, device=target.device)
+    else:
+        _check("tokens", tokens, torch.int32, (N, L1))
+    if accepted is None:
+        accepted = torch.empty((N,), dtype=torch.int32, device=target.device)
+    else:
+        _check("accepted", accepted, torch.int32, (N,))
+    _same_device(target.device, draft=draft, draft_tokens=draft_tokens, uniforms=uniforms,
+                 draft_lens=draft_lens, tokens=tokens, accepted=accepted)
+    L_ = lib()
+    _run_on(target.device, stream, lambda st: L_.kda_verify_tokens(
+        _ptr(target), _ptr(draft), _ptr(draft_tokens), _ptr(uniforms), _ptr(draft_lens),
+        _ptr(tokens), _ptr(accepted), N, L, V, st), "kda_verify_tokens")
+    return tokens, accepted

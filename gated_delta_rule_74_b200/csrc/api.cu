@@ -6,6 +6,8 @@
 #include <initializer_list>
 
 #include "kda_common.cuh"
+#include "latent.cuh"
+#include "latent_attn.cuh"
 
 namespace kda {
 static std::atomic<unsigned long long> g_launches{0};
@@ -15,7 +17,7 @@ void note_launches(unsigned long long n) { g_launches.fetch_add(n, std::memory_o
 namespace {
 
 constexpr int kVersionMajor = 0;
-constexpr int kVersionMinor = 1;
+constexpr int kVersionMinor = 2;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool head_ok(int d) { return d == 64 || d == 128; }
@@ -304,6 +306,154 @@ int kda_chunk_bwd_ws(const void* q, const void* k, const void* v, const float* g
   return chunk_bwd_impl(q, k, v, g, beta, h0, cu_seqlens, dout, dhT, dq, dk, dv, dg, dbeta, dh0,
                         B, T, H, dk_dim, dv_dim, group_shift(g_group, dk_dim), in_dtype, stream,
                         &ws);
+}
+
+// ------------------------------------------------ latent attention, drafted tokens
+namespace {
+int esize(int dtype) { return dtype == KDA_BF16 ? 2 : 4; }
+bool stride_ok(long long s, int dtype) { return s > 0 && s < (1LL << 37) && s * esize(dtype) % 16 == 0; }
+
+// What kda_latent_append and kda_latent_attn check alike.
+int latent_shape_ok(int N, int L, int H, int rank, int rope, int num_pages, int page_size,
+                    int max_pages, long long page_stride, long long row_stride, int dtype,
+                    bool packed) {
+  if (N < 1 || L < 0 || H < 1) return KDA_ERR_INVALID_ARG;
+  if (dtype != KDA_BF16 && dtype != KDA_F32) return KDA_ERR_INVALID_ARG;
+  if (num_pages < 1 || page_size < 1 || max_pages < 1) return KDA_ERR_INVALID_ARG;
+  if (rank < 128 || rank > 512 || rank % 128 != 0 || (rope != 0 && rope != 64))
+    return KDA_ERR_UNSUPPORTED;
+  if (!stride_ok(page_stride, dtype) || !stride_ok(row_stride, dtype) ||
+      row_stride < rank + rope || page_stride < rank + rope)
+    return KDA_ERR_INVALID_ARG;
+  // rows are indexed with 32 bits
+  const long long tokens = packed ? (long long)L : (long long)N * L;
+  if (tokens * H > 0x7fff0000LL || N > (1 << 24)) return KDA_ERR_INVALID_ARG;
+  return KDA_OK;
+}
+
+int latent_attn_impl(const void* q, const void* kv_cache, const int32_t* page_table,
+                     const int32_t* seq_lens, const int32_t* cu_seqlens, void* out, float* lse,
+                     int N, int L, int H, int rank, int rope, int num_pages, int page_size,
+                     int max_pages, long long page_stride, long long row_stride, float scale,
+                     int dtype, void* stream, const kda::Workspace* ws) {
+  const int rc = latent_shape_ok(N, L, H, rank, rope, num_pages, page_size, max_pages, page_stride,
+                                 row_stride, dtype, cu_seqlens != nullptr);
+  if (rc != KDA_OK) return rc;
+  if (L > 0) {
+    if (!pointers_ok({q, kv_cache, page_table, seq_lens, out}, {cu_seqlens, lse}))
+      return KDA_ERR_INVALID_ARG;
+  } else if (!pointers_ok({}, {q, kv_cache, page_table, seq_lens, out, cu_seqlens, lse})) {
+    return KDA_ERR_INVALID_ARG;
+  }
+  const kda::LatentAttnShape sh{N, cu_seqlens ? 0 : L, L, H, rank, rope, num_pages, page_size,
+                                max_pages, page_stride, row_stride, scale};
+  if (ws) {
+    int sms = 0;
+    if (!current_sms(&sms)) return KDA_ERR_CUDA;
+    if (!workspace_ok(ws, kda::latent_attn_scratch_bytes(N, sh.L, L, H, rank, page_size, dtype, sms)))
+      return KDA_ERR_INVALID_ARG;
+  }
+  if (L == 0) return KDA_OK;                        // no new tokens: nothing to write
+  return status_from(kda::launch_latent_attn(q, kv_cache, page_table, seq_lens, cu_seqlens, out,
+                                             lse, sh, dtype, static_cast<cudaStream_t>(stream),
+                                             ws));
+}
+}  // namespace
+
+int kda_latent_append(const void* kv, const float* norm_weight, const float* inv_freq,
+                      const void* q_pe, void* q_pe_out, void* kv_cache,
+                      const int32_t* page_table, const int32_t* seq_lens,
+                      const int32_t* cu_seqlens, int N, int L, int H, int rank, int rope,
+                      int num_pages, int page_size, int max_pages, long long page_stride,
+                      long long row_stride, long long kv_stride, long long q_tok,
+                      long long q_head, long long q_out_tok, long long q_out_head, float eps,
+                      int interleaved, int dtype, void* stream) {
+  const int rc = latent_shape_ok(N, L, H, rank, rope, num_pages, page_size, max_pages, page_stride,
+                                 row_stride, dtype, cu_seqlens != nullptr);
+  if (rc != KDA_OK) return rc;
+  if ((q_pe == nullptr) != (q_pe_out == nullptr)) return KDA_ERR_INVALID_ARG;
+  if (q_pe && rope == 0) return KDA_ERR_INVALID_ARG;
+  if (!(eps >= 0.f)) return KDA_ERR_INVALID_ARG;
+  if (!stride_ok(kv_stride, dtype) || kv_stride < rank + rope) return KDA_ERR_INVALID_ARG;
+  if (q_pe && (!stride_ok(q_tok, dtype) || !stride_ok(q_head, dtype) ||
+               !stride_ok(q_out_tok, dtype) || !stride_ok(q_out_head, dtype)))
+    return KDA_ERR_INVALID_ARG;
+  if (L > 0) {
+    if (!pointers_ok({kv, kv_cache, page_table, seq_lens},
+                     {norm_weight, inv_freq, q_pe, q_pe_out, cu_seqlens}))
+      return KDA_ERR_INVALID_ARG;
+  } else if (!pointers_ok({}, {kv, kv_cache, page_table, seq_lens, norm_weight, inv_freq, q_pe,
+                               q_pe_out, cu_seqlens})) {
+    return KDA_ERR_INVALID_ARG;
+  }
+  if (L == 0) return KDA_OK;
+  kda::LatentAppendShape sh = {};
+  sh.tokens = cu_seqlens ? (long long)L : (long long)N * L;
+  sh.N = N;
+  sh.L = L;
+  sh.H = H;
+  sh.rank = rank;
+  sh.rope = rope;
+  sh.num_pages = num_pages;
+  sh.page_size = page_size;
+  sh.max_pages = max_pages;
+  sh.page_stride = page_stride;
+  sh.row_stride = row_stride;
+  sh.kv_stride = kv_stride;
+  sh.q_tok = q_tok;
+  sh.q_head = q_head;
+  sh.qo_tok = q_out_tok;
+  sh.qo_head = q_out_head;
+  sh.eps = eps;
+  sh.interleaved = interleaved != 0;
+  return status_from(kda::launch_latent_append(kv, norm_weight, inv_freq, q_pe, q_pe_out, kv_cache,
+                                               page_table, seq_lens, cu_seqlens, sh, dtype,
+                                               static_cast<cudaStream_t>(stream)));
+}
+
+int kda_latent_attn(const void* q, const void* kv_cache, const int32_t* page_table,
+                    const int32_t* seq_lens, const int32_t* cu_seqlens, void* out, float* lse,
+                    int N, int L, int H, int rank, int rope, int num_pages, int page_size,
+                    int max_pages, long long page_stride, long long row_stride, float scale,
+                    int dtype, void* stream) {
+  return latent_attn_impl(q, kv_cache, page_table, seq_lens, cu_seqlens, out, lse, N, L, H, rank,
+                          rope, num_pages, page_size, max_pages, page_stride, row_stride, scale,
+                          dtype, stream, nullptr);
+}
+
+int kda_latent_attn_ws(const void* q, const void* kv_cache, const int32_t* page_table,
+                       const int32_t* seq_lens, const int32_t* cu_seqlens, void* out, float* lse,
+                       int N, int L, int H, int rank, int rope, int num_pages, int page_size,
+                       int max_pages, long long page_stride, long long row_stride, float scale,
+                       int dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  const kda::Workspace ws{workspace, workspace_bytes};
+  return latent_attn_impl(q, kv_cache, page_table, seq_lens, cu_seqlens, out, lse, N, L, H, rank,
+                          rope, num_pages, page_size, max_pages, page_stride, row_stride, scale,
+                          dtype, stream, &ws);
+}
+
+int kda_latent_attn_workspace_size(int N, int L, int H, int rank, int rope, int page_size,
+                                   int packed, int dtype, int sms, size_t* bytes) {
+  if (!bytes || sms < 0) return KDA_ERR_INVALID_ARG;
+  const int rc = latent_shape_ok(N, L, H, rank, rope, 1, page_size, 1, rank + rope, rank + rope,
+                                 dtype, packed != 0);
+  if (rc != KDA_OK) return rc;
+  if (sms == 0 && !current_sms(&sms)) return KDA_ERR_CUDA;
+  *bytes = kda::latent_attn_scratch_bytes(N, packed ? 0 : L, L, H, rank, page_size, dtype, sms);
+  return KDA_OK;
+}
+
+int kda_verify_tokens(const float* target, const float* draft, const int32_t* draft_tokens,
+                      const float* uniforms, const int32_t* draft_lens, int32_t* tokens,
+                      int32_t* accepted, int N, int L, int V, void* stream) {
+  if (N < 1 || L < 0 || V < 1 || V > (1 << 30)) return KDA_ERR_INVALID_ARG;
+  if (!pointers_ok({target, uniforms, tokens, accepted}, {draft, draft_tokens, draft_lens}))
+    return KDA_ERR_INVALID_ARG;
+  if (L > 0 && !draft_tokens) return KDA_ERR_INVALID_ARG;
+  if (N > (1 << 24) || (long long)N * (L + 1) > 0x7fffffffLL) return KDA_ERR_INVALID_ARG;
+  return status_from(kda::launch_verify_tokens(target, L > 0 ? draft : nullptr, draft_tokens,
+                                               uniforms, draft_lens, tokens, accepted, N, L, V,
+                                               static_cast<cudaStream_t>(stream)));
 }
 
 int kda_pool_usage(int reset, unsigned long long* used_high_bytes) {

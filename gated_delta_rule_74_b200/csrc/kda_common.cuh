@@ -21,7 +21,8 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(flo
 // Runs setup() (kernel attributes and the like) once per call site and device, with
 // that device current; thread-safe.  A setup that fails is retried on the next call.
 enum OnceSite {
-  kOnceSplit = 0, kOnceTc, kOnceDecodeChunk, kOnceCombine, kOnceCombineImg, kOnceBwdTc, kOnceSites
+  kOnceSplit = 0, kOnceTc, kOnceDecodeChunk, kOnceCombine, kOnceCombineImg, kOnceBwdTc,
+  kOnceLatentSimt, kOnceLatentTc, kOnceSites
 };
 bool once_per_device(int site, bool (*setup)());
 

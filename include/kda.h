@@ -424,6 +424,138 @@ KDA_API int kda_chunk_bwd_ws(const void* q, const void* k, const void* v,
 KDA_API int kda_pool_usage(int reset, unsigned long long* used_high_bytes);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Latent attention beside KDA, and the checking of drafted tokens
+ *
+ * The hybrid that the cards describe has an exact-attention layer for every three KDA
+ * layers, of the latent kind (Kimi-K3-Tiny-L13 card: "9 KDA + 4 MLA mixers"): a token
+ * keeps one vector that all heads share, `rank` latent values and `rope` position values
+ * behind them, in a paged cache.  One serving step of such a layer is kda_latent_append
+ * for the new tokens, then kda_latent_attn; kda_verify_tokens decides which drafted
+ * tokens of a step stand (kda_decode_tokens / kda_decode_chunk advance the KDA layers'
+ * states over the same tokens; run from the state before the step with beta = g = 0 from
+ * the first fallen token on, they leave the state of the accepted prefix).
+ *
+ * Conventions of the three, besides those at the top of this file
+ *   - Sequences: N of them.  cu_seqlens == NULL: L new tokens each, token tensors
+ *     [N, L, ..].  cu_seqlens != NULL (DEVICE int32 [N + 1], as for kda_chunk_fwd): packed,
+ *     L is the number of tokens in all, token tensors [1, L, ..]; rows that belong to no
+ *     sequence are left untouched.
+ *   - seq_lens: DEVICE int32 [N], the tokens each sequence has in the cache WITH its new
+ *     ones (before kda_latent_append has written them, too).  With c new tokens, new
+ *     token i is at position seq_lens[n] - c + i.  A sequence of length 0 is allowed
+ *     (a padding slot), and so is one shorter than c: its first tokens have negative
+ *     positions, which are not written and see nothing.
+ *   - kv_cache: pages of page_size rows of rank + rope values.  Row r of page p starts
+ *     p * page_stride + r * row_stride elements behind the pointer (both strides
+ *     multiples of 16 bytes, row_stride >= rank + rope), so that a layer's slice of a
+ *     larger pool serves as it is.  page_size: any from 1 on.
+ *   - page_table: DEVICE int32 [N, max_pages], the pages of each sequence in order.
+ *     Entries behind a sequence's length are not used.  Lengths, offsets and page ids are
+ *     device memory and are not checked on the host: those out of range (a length beyond
+ *     max_pages * page_size, a page id outside [0, num_pages)) give undefined results for
+ *     that sequence, but every access stays inside the buffers given.
+ *   - rank in {128, 256, 384, 512}, rope in {0, 64}; others: KDA_ERR_UNSUPPORTED.
+ *   - Calls can be captured into CUDA graphs; a replay reads lengths and pages anew.
+ */
+
+/*
+ * kda_latent_append -- norm, rotate and write the new tokens' latent rows to the cache.
+ *
+ *     kv  [.., rank + rope], kv_stride elements from one token to the next
+ *     y[0, rank)  = x[0, rank) * rsqrt(mean(x[0, rank)^2) + eps) * norm_weight
+ *                   (norm_weight fp32 [rank]; NULL: copied)
+ *     y[rank, ..) = x[rank, ..) turned by the angles position * inv_freq[f], f < rope / 2
+ *                   (inv_freq fp32 [rope / 2]; NULL: copied); pair f is elements
+ *                   (f, f + rope / 2), or (2 f, 2 f + 1) with interleaved != 0
+ *     kv_cache[page_table[n][position / page_size]][position % page_size] = y
+ * and, unless q_pe is NULL (it needs rope = 64), the same turn for the queries' position
+ * values: q_pe_out = turned q_pe, [.., H, rope] with q_tok / q_head (q_out_tok /
+ * q_out_head) elements from one token / head to the next; q_pe_out == q_pe is allowed, as
+ * is q_pe_out = the last `rope` columns of the queries that kda_latent_attn takes.
+ * Angles are formed in 64 bits, everything else in fp32, rounded once.
+ * Two tokens of one call must not share a slot.  dtype is the type of kv, q_pe, q_pe_out
+ * and kv_cache.  H is used with q_pe only.
+ * Returns KDA_OK, KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED or KDA_ERR_CUDA.
+ */
+KDA_API int kda_latent_append(const void* kv, const float* norm_weight, const float* inv_freq,
+                              const void* q_pe, void* q_pe_out, void* kv_cache,
+                              const int32_t* page_table, const int32_t* seq_lens,
+                              const int32_t* cu_seqlens, int N, int L, int H, int rank,
+                              int rope, int num_pages, int page_size, int max_pages,
+                              long long page_stride, long long row_stride, long long kv_stride,
+                              long long q_tok, long long q_head, long long q_out_tok,
+                              long long q_out_head, float eps, int interleaved, int dtype,
+                              void* stream);
+
+/*
+ * kda_latent_attn -- absorbed latent attention of each sequence's new tokens over its
+ * cache, causal.
+ *
+ *     q   [.., H, rank + rope]   (the query taken through the keys' up-projection, and its
+ *                                 turned position values)
+ *     s_j = scale * q . c_j over the cached rows j <= the token's position
+ *     out [.., H, rank] = sum_j softmax(s)_j c_j[0, rank)
+ *     lse [.., H] fp32  = log sum_j exp(s_j), or NULL to skip
+ * A token that sees nothing (a negative position) gives out = 0 and lse = -inf.  Rows of
+ * the cache that a token does not see, and what lies behind a sequence's length in its
+ * last page, have no effect on it, infinities and NaN included.  out must not alias any
+ * input.  L = 1 is the decode step, L of a few the check of drafted tokens, any L (or
+ * packed sequences) a prefill chunk behind cached context.
+ *
+ * KDA_BF16 runs on the tensor cores (fp32 accumulation, the softmax in fp32, its weights
+ * rounded to bf16 for the second product) when page_size is a multiple of 8, else on the
+ * CUDA cores; KDA_F32 runs in fp32 on the CUDA cores.  Long sequences are split over the
+ * SMs and joined, in an order that depends on the lengths alone: the same call gives the
+ * same bits.  The split's scratch (kda_latent_attn_workspace_size) comes from the library
+ * pool; kda_latent_attn_ws takes it from the caller instead, on the terms of
+ * kda_chunk_fwd_ws, and allocates nothing.
+ * Returns KDA_OK, KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED or KDA_ERR_CUDA.
+ */
+KDA_API int kda_latent_attn(const void* q, const void* kv_cache, const int32_t* page_table,
+                            const int32_t* seq_lens, const int32_t* cu_seqlens, void* out,
+                            float* lse, int N, int L, int H, int rank, int rope, int num_pages,
+                            int page_size, int max_pages, long long page_stride,
+                            long long row_stride, float scale, int dtype, void* stream);
+KDA_API int kda_latent_attn_ws(const void* q, const void* kv_cache, const int32_t* page_table,
+                               const int32_t* seq_lens, const int32_t* cu_seqlens, void* out,
+                               float* lse, int N, int L, int H, int rank, int rope,
+                               int num_pages, int page_size, int max_pages,
+                               long long page_stride, long long row_stride, float scale,
+                               int dtype, void* workspace, size_t workspace_bytes, void* stream);
+/* Workspace bytes of such a call on a device with `sms` streaming multiprocessors (0: the
+ * current device's); packed != 0: with cu_seqlens. */
+KDA_API int kda_latent_attn_workspace_size(int N, int L, int H, int rank, int rope,
+                                           int page_size, int packed, int dtype, int sms,
+                                           size_t* bytes);
+
+/*
+ * kda_verify_tokens -- which drafted tokens stand, and the token after them.
+ *
+ *     target [N, L + 1, V] fp32: the target's probabilities before each drafted token and
+ *                                after the last
+ *     draft  [N, L, V] fp32: the probabilities the drafts were drawn from; NULL: each
+ *                            drafted token was certain (found by a lookup, or greedy)
+ *     draft_tokens int32 [N, L], uniforms fp32 [N, L + 1] in [0, 1)
+ *     draft_lens int32 [N]: drafts of each sequence, 0 .. L (NULL: L; clamped)
+ * Draft i of sequence n stands while uniforms[i] * draft[i][x_i] < target[i][x_i] (strict;
+ * without `draft`, uniforms[i] < target[i][x_i]); a token outside [0, V) falls.  Let a be
+ * the number before the first that falls.  Token a is drawn by uniforms[L] from the
+ * weights max(target[a] - draft[a], 0) after a fall (without `draft`: target[a] without
+ * x_a), else from target[a]: the first v whose running sum exceeds uniforms[L] times the
+ * sum of all (rows need not sum to one).  If no weight is positive, the fallen draft is
+ * kept as token a (target and draft rows are then equal), or -1 if there is none.
+ *     tokens int32 [N, L + 1]: x_0 .. x_{a-1}, token a, then -1    accepted int32 [N]: a
+ * Products and sums are taken in 64 bits.  Reads of the N * (2 L + 1) rows only those it
+ * needs.  N >= 1, L >= 0 (draft, draft_tokens may be NULL at 0), 1 <= V <= 2^30.
+ * Returns KDA_OK, KDA_ERR_INVALID_ARG or KDA_ERR_CUDA.
+ */
+KDA_API int kda_verify_tokens(const float* target, const float* draft,
+                              const int32_t* draft_tokens, const float* uniforms,
+                              const int32_t* draft_lens, int32_t* tokens, int32_t* accepted,
+                              int N, int L, int V, void* stream);
+
+/*
  * kda_device_status -- did a bounded device-side wait give up?
  *
  * Every wait of the library's kernels on an asynchronous copy or a tensor-core
@@ -492,7 +624,10 @@ typedef enum {
   KDA_KERNEL_BWD_PREP = 7,      /* chunked backward: per-chunk prep               */
   KDA_KERNEL_BWD_CHAIN = 8,     /* chunked backward: forward and reverse chains   */
   KDA_KERNEL_BWD_GRAD = 9,      /* chunked backward: per-chunk gradients          */
-  KDA_KERNEL_KINDS = 10
+  KDA_KERNEL_LATENT_APPEND = 10, /* latent rows into the paged cache              */
+  KDA_KERNEL_LATENT_ATTN = 11,  /* latent attention and its join                  */
+  KDA_KERNEL_VERIFY = 12,       /* check of drafted tokens                        */
+  KDA_KERNEL_KINDS = 13
 } kda_kernel_kind_t;
 KDA_API int kda_timing_start(void);
 KDA_API int kda_timing_stop(void);
