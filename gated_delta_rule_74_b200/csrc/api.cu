@@ -1,5 +1,6 @@
 // C ABI of libkda: host-side argument validation and kernel dispatch.
 // The entry points and their contracts are declared and documented in kda.h.
+#include <float.h>
 #include <stdint.h>
 
 #include <atomic>
@@ -339,6 +340,7 @@ int latent_attn_impl(const void* q, const void* kv_cache, const int32_t* page_ta
   const int rc = latent_shape_ok(N, L, H, rank, rope, num_pages, page_size, max_pages, page_stride,
                                  row_stride, dtype, cu_seqlens != nullptr);
   if (rc != KDA_OK) return rc;
+  if (!(scale > 0.f) || scale > FLT_MAX) return KDA_ERR_INVALID_ARG;
   if (L > 0) {
     if (!pointers_ok({q, kv_cache, page_table, seq_lens, out}, {cu_seqlens, lse}))
       return KDA_ERR_INVALID_ARG;
@@ -466,7 +468,8 @@ int kda_device_status(int reset) {
   int any = 0;
   for (auto take : {kda::take_split_timeout, kda::take_tc_timeout, kda::take_bwd_timeout,
                     kda::take_bwd_tc_timeout, kda::take_combine_timeout,
-                    kda::take_selftest_timeout, kda::take_decode_chunk_timeout}) {
+                    kda::take_selftest_timeout, kda::take_decode_chunk_timeout,
+                    kda::take_latent_timeout}) {
     int f = 0;
     if (take(&f, reset != 0) != cudaSuccess) return status_from(cudaErrorUnknown);
     any |= f;

@@ -147,6 +147,7 @@ cudaError_t take_bwd_tc_timeout(int* flag, bool reset);
 cudaError_t take_combine_timeout(int* flag, bool reset);
 cudaError_t take_selftest_timeout(int* flag, bool reset);
 cudaError_t take_decode_chunk_timeout(int* flag, bool reset);
+cudaError_t take_latent_timeout(int* flag, bool reset);
 
 // Multi-token decode in the chunked form on the tensor cores (bf16, dk = dv = 128,
 // 1 <= L <= 16 tokens per (sequence, head)).

@@ -13,6 +13,7 @@
 // Bound by shared-memory reads (each FMA's operands come from there), not by the cache's
 // bytes; fp32 has no tensor-core form of fp32 accuracy.
 #include "latent_attn.cuh"
+#include "sm100.cuh"
 
 namespace kda {
 namespace {
@@ -176,9 +177,30 @@ kda_latent_simt_kernel(const T* __restrict__ q, const T* __restrict__ cache,
 
 // ---------------------------------------------------------------------------
 // Join: row = sum_c e^(lse_c - M) o_c / sum_c e^(lse_c - M) over the CTAs that share the
-// row's block, in their order.  One unit a row; 512 threads: four runs of CTAs, 128 threads
-// of four columns each.
+// row's block, in their order.  Bound by latency (the partial results are in L2): a block's
+// four groups of 128 threads take a row each while few CTAs share it, all loads at once,
+// and a quarter of the CTAs each where many do.
 constexpr int kJT = 512;
+constexpr int kFew = 8;
+
+// Partial slot of the i-th CTA of a shared block that starts in CTA c0.
+__device__ __forceinline__ long long join_slot(int c0, int i) {
+  return i == 0 ? 2 * c0 + 1 : 2 * (c0 + i);
+}
+template <typename T>
+__device__ __forceinline__ void join_store(T* o, const float4& a) {
+  o[0] = from_f32<T>(a.x);
+  o[1] = from_f32<T>(a.y);
+  o[2] = from_f32<T>(a.z);
+  o[3] = from_f32<T>(a.w);
+}
+__device__ __forceinline__ void join_add(float4& a, float w, const float4& v) {
+  if (w == 0.f) return;                              // nothing seen: nothing taken
+  a.x = fmaf(w, v.x, a.x);
+  a.y = fmaf(w, v.y, a.y);
+  a.z = fmaf(w, v.z, a.z);
+  a.w = fmaf(w, v.w, a.w);
+}
 
 template <typename T>
 __global__ void __launch_bounds__(kJT)
@@ -187,14 +209,19 @@ kda_latent_join_kernel(T* __restrict__ out, float* __restrict__ lse, LatentParti
   __shared__ int s_off[kLatentMaxCtas + 1];
   __shared__ float s_w[kLatentMaxCtas];
   __shared__ float4 s_part[3][128];
-  __shared__ int s_carry;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // rows of the CTAs' shared blocks before each CTA
+  const int g = tid >> 7, d4 = tid & 127;
+  sm100::grid_dep_wait();
+  // units (rows, or four rows) of the CTAs' shared blocks before each CTA
   if (warp == 0) {
     int run = 0;
     for (int c0 = 0; c0 < G; c0 += 32) {
       const int c = c0 + lane;
-      const int v = c < G ? pt.head[c].y : 0;
+      int v = 0;
+      if (c < G) {
+        const int4 hd = pt.head[c];
+        v = hd.z - c + 1 <= kFew ? (hd.y + 3) / 4 : hd.y;
+      }
       int s = v;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -204,10 +231,10 @@ kda_latent_join_kernel(T* __restrict__ out, float* __restrict__ lse, LatentParti
       if (c < G) s_off[c] = run + s - v;
       run += __shfl_sync(0xffffffffu, s, 31);
     }
-    if (lane == 0) s_carry = run;
+    if (lane == 0) s_off[G] = run;
   }
   __syncthreads();
-  const int units = s_carry;
+  const int units = s_off[G];
   for (int u = blockIdx.x; u < units; u += gridDim.x) {
     int lo = 0, hi = G - 1;                            // the last CTA that starts at or before u
     while (lo < hi) {
@@ -215,44 +242,61 @@ kda_latent_join_kernel(T* __restrict__ out, float* __restrict__ lse, LatentParti
       if (s_off[mid] <= u) lo = mid;
       else hi = mid - 1;
     }
-    const int c0 = lo, r = u - s_off[c0];
+    const int c0 = lo;
     const int4 hd = pt.head[c0];
     const int k = hd.z - c0 + 1;
-    __syncthreads();                                   // s_w and s_part of the row before are read
-    // slot of run element i: the first CTA's ending block, the others' beginning ones
-    for (int i = tid; i < k; i += kJT)
-      s_w[i] = pt.lse[(long long)(i == 0 ? 2 * c0 + 1 : 2 * (c0 + i)) * nr + r];
-    __syncthreads();
-    float M = -INFINITY;
-    bool nan = false;
-    for (int i = lane; i < k; i += 32) {
-      M = fmaxf(M, s_w[i]);
-      nan = nan || s_w[i] != s_w[i];
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    if (__any_sync(0xffffffffu, nan)) M = NAN;
-    const float Ms = M == -INFINITY ? 0.f : M;
-    float z = 0.f;
-    for (int i = 0; i < k; ++i) z += expf(s_w[i] - Ms);
-    const float inv = z == 0.f ? 0.f : 1.0f / z;
-    if (tid == 0 && lse) lse[hd.x + r] = z == 0.f ? -INFINITY : Ms + logf(z);
-    const int g = tid >> 7, d4 = tid & 127;
-    const int i0 = k * g / 4, i1 = k * (g + 1) / 4;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (d4 * 4 < rank) {
-#pragma unroll 4
-      for (int i = i0; i < i1; ++i) {
-        const float w = expf(s_w[i] - Ms) * inv;
-        const float4 v = *reinterpret_cast<const float4*>(
-            pt.o + ((long long)(i == 0 ? 2 * c0 + 1 : 2 * (c0 + i)) * nr + r) * rank + d4 * 4);
-        if (w != 0.f) {                                // nothing seen: nothing taken
-          a.x = fmaf(w, v.x, a.x);
-          a.y = fmaf(w, v.y, a.y);
-          a.z = fmaf(w, v.z, a.z);
-          a.w = fmaf(w, v.w, a.w);
+    if (k <= kFew) {
+      const int r = 4 * (u - s_off[c0]) + g;
+      if (r >= hd.y) continue;
+      float w[kFew];
+      float4 v[kFew];
+#pragma unroll
+      for (int i = 0; i < kFew; ++i) {
+        w[i] = -INFINITY;
+        if (i < k) {
+          const long long at = join_slot(c0, i) * nr + r;
+          w[i] = pt.lse[at];
+          if (d4 * 4 < rank) v[i] = *reinterpret_cast<const float4*>(pt.o + at * rank + d4 * 4);
         }
       }
+      float M = -INFINITY, z = 0.f;
+#pragma unroll
+      for (int i = 0; i < kFew; ++i) M = fmaxf(M, w[i]);
+      const float Ms = M == -INFINITY ? 0.f : M;
+#pragma unroll
+      for (int i = 0; i < kFew; ++i) z += expf(w[i] - Ms);   // a NaN makes all of it one
+      const float inv = z == 0.f ? 0.f : 1.0f / z;
+      if (d4 == 0 && lse) lse[hd.x + r] = z == 0.f ? -INFINITY : Ms + logf(z);
+      if (d4 * 4 < rank) {
+#pragma unroll
+        for (int i = 0; i < kFew; ++i)
+          if (i < k) join_add(a, expf(w[i] - Ms) * inv, v[i]);
+        join_store(out + (long long)(hd.x + r) * rank + d4 * 4, a);
+      }
+      continue;
+    }
+    const int r = u - s_off[c0];
+    __syncthreads();                                   // s_w and s_part of the row before are read
+    for (int i = tid; i < k; i += kJT) s_w[i] = pt.lse[join_slot(c0, i) * nr + r];
+    __syncthreads();
+    float M = -INFINITY;
+    for (int i = lane; i < k; i += 32) M = fmaxf(M, s_w[i]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float Ms = M == -INFINITY ? 0.f : M;
+    float z = 0.f;
+    for (int i = lane; i < k; i += 32) z += expf(s_w[i] - Ms);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+    const float inv = z == 0.f ? 0.f : 1.0f / z;
+    if (tid == 0 && lse) lse[hd.x + r] = z == 0.f ? -INFINITY : Ms + logf(z);
+    const int i0 = k * g / 4, i1 = k * (g + 1) / 4;
+    if (d4 * 4 < rank) {
+#pragma unroll 8
+      for (int i = i0; i < i1; ++i)
+        join_add(a, expf(s_w[i] - Ms) * inv,
+                 *reinterpret_cast<const float4*>(pt.o + (join_slot(c0, i) * nr + r) * rank + d4 * 4));
     }
     if (g > 0) s_part[g - 1][d4] = a;
     __syncthreads();
@@ -265,11 +309,7 @@ kda_latent_join_kernel(T* __restrict__ out, float* __restrict__ lse, LatentParti
         a.z += v.z;
         a.w += v.w;
       }
-      T* o = out + (long long)(hd.x + r) * rank + d4 * 4;
-      o[0] = from_f32<T>(a.x);
-      o[1] = from_f32<T>(a.y);
-      o[2] = from_f32<T>(a.z);
-      o[3] = from_f32<T>(a.w);
+      join_store(out + (long long)(hd.x + r) * rank + d4 * 4, a);
     }
   }
 }
@@ -287,19 +327,37 @@ cudaError_t run_simt(const void* q, const void* cache, const int32_t* page_table
                 static_cast<T*>(out), lse, sh, pt));
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  KDA_TIMED(KDA_KERNEL_LATENT_ATTN, stream,
-            kda_latent_join_kernel<T><<<G, kJT, 0, stream>>>(static_cast<T*>(out), lse, pt, G,
-                                                             kRows, sh.rank));
-  note_launches(2);
-  return cudaGetLastError();
+  note_launches(1);
+  return launch_latent_join(out, lse, pt, G, kRows, sh.rank,
+                            sizeof(T) == 2 ? KDA_BF16 : KDA_F32, stream);
 }
 
 int simt_ctas(int sms) { return 2 * sms < kLatentMaxCtas ? 2 * sms : kLatentMaxCtas; }
 
 }  // namespace
 
+// Four join blocks an SM are resident; more would only wait.
+cudaError_t launch_latent_join(void* out, float* lse, const LatentPartials& pt, int G, int nr,
+                               int rank, int dtype, cudaStream_t stream) {
+  int sms = 0;
+  if (!device_ctx(&sms, nullptr)) return cudaErrorInvalidDevice;
+  cudaError_t e = cudaSuccess;
+  if (dtype == KDA_BF16)
+    KDA_TIMED(KDA_KERNEL_LATENT_ATTN, stream,
+              e = launch_after(kda_latent_join_kernel<__nv_bfloat16>, dim3(4 * sms), dim3(kJT), 0,
+                               stream, static_cast<__nv_bfloat16*>(out), lse, pt, G, nr, rank));
+  else
+    KDA_TIMED(KDA_KERNEL_LATENT_ATTN, stream,
+              e = launch_after(kda_latent_join_kernel<float>, dim3(4 * sms), dim3(kJT), 0, stream,
+                               static_cast<float*>(out), lse, pt, G, nr, rank));
+  note_launches(1);
+  return e;
+}
+
 size_t latent_attn_scratch_bytes(int N, int L, int T, int H, int rank, int page_size, int dtype,
                                  int sms) {
+  if (latent_tc_supported(dtype, page_size))
+    return latent_tc_scratch_bytes(N, L, T, H, rank, sms);
   return latent_scratch_bytes(simt_ctas(sms), kRows, rank);
 }
 
@@ -331,7 +389,10 @@ cudaError_t launch_latent_attn(const void* q, const void* cache, const int32_t* 
   }
   const int G = simt_ctas(sms);
   const LatentPartials pt = latent_partials(buf, G, kRows);
-  e = dtype == KDA_BF16 ? run_simt<__nv_bfloat16>(q, cache, page_table, seq_lens, cu_seqlens, out,
+  if (latent_tc_supported(dtype, sh.page_size))
+    e = launch_latent_tc(q, cache, page_table, seq_lens, cu_seqlens, out, lse, sh, sms, buf, stream);
+  else
+    e = dtype == KDA_BF16 ? run_simt<__nv_bfloat16>(q, cache, page_table, seq_lens, cu_seqlens, out,
                                                   lse, sh, G, pt, stream)
                         : run_simt<float>(q, cache, page_table, seq_lens, cu_seqlens, out, lse, sh,
                                           G, pt, stream);

@@ -53,6 +53,16 @@ cudaError_t launch_latent_attn(const void* q, const void* cache, const int32_t* 
                                float* lse, const LatentAttnShape& sh, int dtype,
                                cudaStream_t stream, const Workspace* ws);
 
+// The tensor-core kernel (latent_attn_tc.cu): bf16, pages of a multiple of 8 rows.
+bool latent_tc_supported(int dtype, int page_size);
+size_t latent_tc_scratch_bytes(int N, int L, int T, int H, int rank, int sms);
+cudaError_t launch_latent_tc(const void* q, const void* cache, const int32_t* page_table,
+                             const int32_t* seq_lens, const int32_t* cu_seqlens, void* out,
+                             float* lse, const LatentAttnShape& sh, int sms, void* buf,
+                             cudaStream_t stream);
+cudaError_t launch_latent_join(void* out, float* lse, const LatentPartials& pt, int G, int nr,
+                               int rank, int dtype, cudaStream_t stream);
+
 // ------------------------------------------------------------------ device side
 // sum_{i < n} floor((a i + b) / m), a, b >= 0, m > 0
 __device__ inline long long floor_sum(long long n, long long m, long long a, long long b) {

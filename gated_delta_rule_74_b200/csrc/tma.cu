@@ -29,14 +29,14 @@ EncodeTiled encoder() {
 
 }  // namespace
 
-bool make_tile_map_3d(CUtensorMap* map, bool fp32, const void* base, uint64_t d0, uint64_t d1,
+static bool encode_3d(CUtensorMap* map, bool fp32, const void* base, uint64_t d0, uint64_t d1,
                       uint64_t d2, uint64_t stride1, uint64_t stride2, uint32_t box0,
-                      uint32_t box2, bool swizzle128) {
+                      uint32_t box1, uint32_t box2, bool swizzle128) {
   const EncodeTiled enc = encoder();
   if (!enc || !base) return false;
   const cuuint64_t dims[3] = {d0, d1, d2};
   const cuuint64_t strides[2] = {stride1, stride2};
-  const cuuint32_t box[3] = {box0, 1u, box2};
+  const cuuint32_t box[3] = {box0, box1, box2};
   const cuuint32_t elem[3] = {1u, 1u, 1u};
   const CUresult r =
       enc(map, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
@@ -44,6 +44,17 @@ bool make_tile_map_3d(CUtensorMap* map, bool fp32, const void* base, uint64_t d0
           swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
+}
+
+bool make_tile_map_3d(CUtensorMap* map, bool fp32, const void* base, uint64_t d0, uint64_t d1,
+                      uint64_t d2, uint64_t stride1, uint64_t stride2, uint32_t box0,
+                      uint32_t box2, bool swizzle128) {
+  return encode_3d(map, fp32, base, d0, d1, d2, stride1, stride2, box0, 1u, box2, swizzle128);
+}
+
+bool make_row_map_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
+                     uint64_t stride1, uint64_t stride2, uint32_t box0, uint32_t box1) {
+  return encode_3d(map, false, base, d0, d1, d2, stride1, stride2, box0, box1, 1u, true);
 }
 
 }  // namespace kda

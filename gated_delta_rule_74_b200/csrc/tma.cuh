@@ -19,4 +19,8 @@ bool make_tile_map_3d(CUtensorMap* map, bool fp32, const void* base, uint64_t d0
                       uint64_t d2, uint64_t stride1, uint64_t stride2, uint32_t box0,
                       uint32_t box2, bool swizzle128);
 
+// The same with boxes of box0 x box1 x 1 elements: runs of d1 rows (128-byte swizzle, bf16).
+bool make_row_map_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
+                     uint64_t stride1, uint64_t stride2, uint32_t box0, uint32_t box1);
+
 }  // namespace kda

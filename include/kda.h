@@ -494,7 +494,7 @@ KDA_API int kda_latent_append(const void* kv, const float* norm_weight, const fl
  *
  *     q   [.., H, rank + rope]   (the query taken through the keys' up-projection, and its
  *                                 turned position values)
- *     s_j = scale * q . c_j over the cached rows j <= the token's position
+ *     s_j = scale * q . c_j over the cached rows j <= the token's position (scale > 0)
  *     out [.., H, rank] = sum_j softmax(s)_j c_j[0, rank)
  *     lse [.., H] fp32  = log sum_j exp(s_j), or NULL to skip
  * A token that sees nothing (a negative position) gives out = 0 and lse = -inf.  Rows of

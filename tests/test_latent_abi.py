@@ -38,7 +38,8 @@ SHAPE = [dict(N=0), dict(Lt=-1), dict(H=0), dict(dt=2), dict(pages=0), dict(page
 
 
 @pytest.mark.parametrize("bad", SHAPE + [dict(q=None), dict(out=None), dict(out=P + 2),
-                                         dict(lse=P + 4)])
+                                         dict(lse=P + 4), dict(scale=0.0),
+                                         dict(scale=float("nan")), dict(scale=float("inf"))])
 def test_attn_rejects_invalid(L, bad):
     assert _attn(L, **bad) == kda.KDA_ERR_INVALID_ARG
 
