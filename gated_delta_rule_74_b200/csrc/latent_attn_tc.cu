@@ -16,15 +16,17 @@
 // memory and tensor cores at 96 rows.  The MMAs stage A and B in shared memory; at N = 64
 // reading them takes 48 of the 128-byte cycles that the 32 of the product would leave.
 //
-// One CTA an SM, its stretch of tiles as latent_attn.cuh lays it out.  Warp 0 brings the
-// tiles by TMA into a ring of slots (128 columns x 64 rows, the rope columns apart), one box
-// a run of rows inside of a page; warp 1 issues the MMAs; warps 4..7 do the softmax (thread =
-// row), the rare rescaling of O^T and the results (thread = value column).  The maximum that
-// the weights refer to moves only when a row's passes it by 2^8, so that O^T is rescaled a
-// few times a sequence; the weights stay below 2^8, far inside of bf16 and fp32.
-// The scores of tile t + 1 are issued while tile t's softmax runs, as far as slots allow
-// (all of them up to 64 rows, the rope and half of the rank at 96); whichever of "the next slot is
-// there" and "the weights are there" comes first goes first.
+// One CTA an SM, its stretch of tiles as latent_attn.cuh lays it out.  Warps 0 and 2 bring
+// the tiles by TMA into a ring of stages (256 columns x 64 rows; the rope columns apart), one
+// box a run of rows inside of a page, warp 3 Q; warp 1 issues the MMAs; warps 4..11 do the
+// softmax (thread = row, two warps a lane quarter with half of the columns each), the rare
+// rescaling of O^T and the results (thread = value column).  The maximum that the weights
+// refer to moves only when a row's passes it by 2^8, so that O^T is rescaled a few times a
+// sequence; the weights stay below 2^8, far inside of bf16 and fp32.
+// The scores of tile t + 1 are issued while tile t's softmax runs, as far as stages allow
+// (all of them up to 64 rows, half of the columns at 96); whichever of "the next stage is
+// there" and "the weights are there" comes first goes first.  A wait between MMAs costs
+// their warp 300 to 450 cycles, as long as eight of the MMAs take, so stages are large.
 //
 // Rows of the tile that some query row does not see (the causal edge, what lies behind the
 // length in the last page) have weights of exactly zero; their infinities and NaN would
@@ -43,42 +45,46 @@ namespace {
 using namespace sm100;
 using bf16 = __nv_bfloat16;
 
-constexpr int kTcThreads = 256;
+constexpr int kTcThreads = 384;
+constexpr int kSoft = 256;                         // threads of warps 4..11
 constexpr int kTcTile = 64;
 constexpr int kTcMaxRows = 96;
 constexpr uint32_t kChunk = 64 * 128;              // 64 cached rows x 64 columns
-constexpr uint32_t kSlot = 2 * kChunk;
-constexpr int kMaxSlots = 12;
-constexpr uint32_t kTcSmem = 229376;               // Q, slots, P; + 1024 for the alignment
+constexpr uint32_t kPair = 2 * kChunk;
+constexpr int kMaxStages = 8;
+constexpr uint32_t kTcSmem = 229376;               // Q, stages, P; + 1024 for the alignment
 constexpr uint32_t kTmemCols = 512, kTmemS = 384;
-constexpr uint32_t kWaitLimit = 1u << 22, kPollLimit = 1u << 26;
+constexpr uint32_t kWaitLimit = 1u << 22, kPollLimit = 1u << 26, kDrainLimit = 1u << 14;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // How shared memory is divided, from the block's rows and the row's columns.
 struct TcPlan {
   int nr;                           // rows of a block, a multiple of 16 up to 96
   int npair;                        // rank / 128
+  int spair, ns;                    // pairs of a stage, stages of a tile
   int nq, np;                       // Q and P buffers
-  int slots, rope_slots;
+  int stages, rope_slots;
   uint32_t q_bytes, p_bytes;
   int box_rows, groups;             // rows of a TMA box; boxes for 64 rows of one chunk
 };
 
 // Q is buffered twice while it is small (a decode step changes blocks every few tiles), P
-// while the slots then still hold two tiles.
+// and the rope columns while the stages then still hold two tiles.
 TcPlan tc_plan(int nr, int rank, int rope, int page_size) {
   TcPlan p;
   p.nr = nr;
   p.npair = rank / 128;
+  p.spair = p.npair < 2 ? 1 : 2;
+  p.ns = (p.npair + 1) / 2;
   p.q_bytes = (uint32_t)nr * (rank + rope) * 2;
   p.p_bytes = (uint32_t)nr * 128;
   p.nq = nr <= 32 ? 2 : 1;
   p.np = nr <= 64 ? 2 : 1;
-  const uint32_t left = kTcSmem - p.nq * p.q_bytes - p.np * p.p_bytes;
+  const uint32_t left = kTcSmem - p.nq * p.q_bytes - p.np * p.p_bytes, stage = p.spair * kPair;
   p.rope_slots = rope ? 2 : 0;
-  if (rope && (int)((left - 2 * kChunk) / kSlot) < 2 * p.npair) p.rope_slots = 1;
-  p.slots = (int)((left - p.rope_slots * kChunk) / kSlot);
-  if (p.slots > kMaxSlots) p.slots = kMaxSlots;
+  if (rope && (int)((left - 2 * kChunk) / stage) < 2 * p.ns) p.rope_slots = 1;
+  p.stages = (int)((left - p.rope_slots * kChunk) / stage);
+  if (p.stages > kMaxStages) p.stages = kMaxStages;
   p.box_rows = kTcTile;
   while (page_size % p.box_rows) p.box_rows /= 2;
   p.groups = kTcTile / p.box_rows;
@@ -87,9 +93,9 @@ TcPlan tc_plan(int nr, int rank, int rope, int page_size) {
 
 struct TcBars {
   uint64_t q_full[2], q_empty[2];
-  uint64_t full[kMaxSlots], empty[kMaxSlots];
-  uint64_t rope_full[2], rope_empty[2];
-  uint64_t s_full[2], s_empty[2];
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t rope_empty[2];
+  uint64_t s_full[2];
   uint64_t p_full[2], pv_done[2];
   uint64_t o_empty, drain;
 };
@@ -108,6 +114,7 @@ __device__ __forceinline__ uint32_t zero_bad(uint32_t w) {     // two bf16: inf,
 __global__ void __launch_bounds__(kTcThreads, 1)
 kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                      const __grid_constant__ CUtensorMap c_map,
+                     const __grid_constant__ CUtensorMap r_map,
                      const int32_t* __restrict__ page_table,
                      const int32_t* __restrict__ seq_lens,
                      const int32_t* __restrict__ cu_seqlens, bf16* __restrict__ out,
@@ -117,14 +124,16 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
   __shared__ LatentStart st;
   __shared__ long long s_sum[33];
   __shared__ float s_row[kTcMaxRows];               // rescaling factors, then 1 / sum
+  __shared__ float s_half[2][kTcMaxRows];           // the column halves' maxima, then sums
   __shared__ uint32_t s_tmem;
   uint8_t* const sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                  ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int nr = pl.nr, npair = pl.npair;
+  const uint32_t stage_bytes = pl.spair * kPair;
   uint8_t* const sq = sm;
-  uint8_t* const sslot = sq + pl.nq * pl.q_bytes;
-  uint8_t* const srope = sslot + pl.slots * kSlot;
+  uint8_t* const sst = sq + pl.nq * pl.q_bytes;
+  uint8_t* const srope = sst + pl.stages * stage_bytes;
   uint8_t* const sp = srope + pl.rope_slots * kChunk;
 
   if (warp == 1) {
@@ -135,18 +144,16 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.q_full[i], 1);
       mbar_init(&bar.q_empty[i], 1);
-      mbar_init(&bar.rope_full[i], 1);
       mbar_init(&bar.rope_empty[i], 1);
       mbar_init(&bar.s_full[i], 1);
-      mbar_init(&bar.s_empty[i], 4);
-      mbar_init(&bar.p_full[i], 4);
+      mbar_init(&bar.p_full[i], kSoft / 32);
       mbar_init(&bar.pv_done[i], 1);
     }
-    for (int i = 0; i < kMaxSlots; ++i) {
-      mbar_init(&bar.full[i], 1);
+    for (int i = 0; i < kMaxStages; ++i) {
+      mbar_init(&bar.full[i], 2);                   // warps 0 and 2
       mbar_init(&bar.empty[i], 1);
     }
-    mbar_init(&bar.o_empty, 4);
+    mbar_init(&bar.o_empty, kSoft / 32);
     mbar_init(&bar.drain, 1);
     fence_mbar_init();
     pt.head[blockIdx.x] = make_int4(0, 0, 0, 0);
@@ -157,183 +164,232 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
   tc_fence_after();
   const uint32_t tb = s_tmem;
   grid_dep_launch();                                // the join may be made ready
-  const int qblocks = (sh.rank + sh.rope) / 64;
   const bool rope = sh.rope != 0;
   bool ok = true;
+  constexpr uint32_t kAll = 0xffffffffu;
 
-  if (warp == 0) {
+  if (warp == 0 || warp == 2) {
     // ------------------------------------------------------------- tiles by TMA
+    // Warp 0 brings the first pair of each stage, warp 2 the second and the rope columns.
+    const int w = warp >> 1;
     LatentWalk walk(st);
     LatentPiece p;
-    uint32_t it = 0, slot = 0, slot_use = 0, rt = 0;     // blocks, pair slots, rope slots so far
+    uint32_t stage = 0, use = 0, rs = 0, ruse = 0;
+    const uint32_t step = pl.box_rows * 128;
     while (ok && walk.next(sh, seq_lens, cu_seqlens, nr, kTcTile, &p)) {
-      const uint32_t qi = it % pl.nq, quse = it / pl.nq;
-      ++it;
-      if (quse > 0) ok = mbar_wait(&bar.q_empty[qi], (quse - 1) & 1, kWaitLimit);
-      if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-      if (lane == 0) {
+      // lane's box of tile t: rows [64 t + lane box_rows, ..) of the sequence; a page past the
+      // cache (zeros) where there is none
+      auto look = [&](int t) {
+        const int pos = t * kTcTile + lane * pl.box_rows;
+        if (lane >= pl.groups || t >= p.t1 || pos >= p.len) return sh.num_pages;
+        const int id = __ldg(page_table + (long long)p.n * sh.max_pages + pos / sh.page_size);
+        return id >= 0 && id < sh.num_pages ? id : sh.num_pages;
+      };
+      int next_page = look(p.t0);
+      for (int t = p.t0; t < p.t1 && ok; ++t) {
+        const int page = next_page, row = (t * kTcTile + lane * pl.box_rows) % sh.page_size;
+        next_page = look(t + 1);
+        for (int s = 0; s < pl.ns; ++s) {
+          if (use > 0) ok = __all_sync(kAll, mbar_wait(&bar.empty[stage], (use - 1) & 1, kWaitLimit));
+          const bool with_rope = rope && w == 1 && s == 0;
+          if (with_rope && ruse > 0)
+            ok = ok && __all_sync(kAll, mbar_wait(&bar.rope_empty[rs], (ruse - 1) & 1, kWaitLimit));
+          if (!ok) break;
+          const int pair = s * pl.spair + w;
+          const bool some = w < pl.spair && pair < npair;
+          uint8_t* const d = sst + stage * stage_bytes + w * kPair;
+          uint8_t* const dr = srope + rs * kChunk;
+          uint64_t* const full = &bar.full[stage];
+          if (elect_one())
+            mbar_arrive_expect_tx(full, (some ? kPair : 0u) + (with_rope ? kChunk : 0u));
+          __syncwarp();
+          for (int b = 0; b < pl.groups; ++b) {
+            const int pg = __shfl_sync(kAll, page, b), rw = __shfl_sync(kAll, row, b);
+            if (elect_one()) {
+              if (with_rope) tma_load_4d(dr + b * step, &r_map, 0, rw, 2 * npair, pg, full);
+              if (some && pl.groups == 1) {
+                tma_load_4d(d, &c_map, 0, rw, 2 * pair, pg, full);
+              } else if (some) {                         // a chunk's boxes lie 64 rows apart
+                tma_load_4d(d + b * step, &r_map, 0, rw, 2 * pair, pg, full);
+                tma_load_4d(d + b * step + kChunk, &r_map, 0, rw, 2 * pair + 1, pg, full);
+              }
+            }
+            __syncwarp();
+          }
+          if (with_rope && ++rs == (uint32_t)pl.rope_slots) {
+            rs = 0;
+            ++ruse;
+          }
+          if (++stage == (uint32_t)pl.stages) {
+            stage = 0;
+            ++use;
+          }
+        }
+      }
+    }
+    // let copies in flight land before the memory goes away (those that never started cost
+    // the limit)
+    for (uint32_t i = 0; !ok && i < (uint32_t)pl.stages; ++i) {
+      const uint32_t uses = use + (i < stage ? 1 : 0);
+      if (uses) mbar_wait(&bar.full[i], (uses - 1) & 1, kDrainLimit);
+    }
+  } else if (warp == 3) {
+    // ------------------------------------------------------------- Q by TMA
+    LatentWalk walk(st);
+    LatentPiece p;
+    uint32_t qi = 0, quse = 0;
+    while (ok && walk.next(sh, seq_lens, cu_seqlens, nr, kTcTile, &p)) {
+      if (quse > 0) ok = __all_sync(kAll, mbar_wait(&bar.q_empty[qi], (quse - 1) & 1, kWaitLimit));
+      if (!ok) break;
+      if (elect_one()) {
         mbar_arrive_expect_tx(&bar.q_full[qi], pl.q_bytes);
-        for (int c = 0; c < qblocks; ++c)
-          tma_load_3d(sq + qi * pl.q_bytes + c * nr * 128, &q_map, 64 * c, (int)p.row0, 0,
-                      &bar.q_full[qi]);
+        tma_load_4d(sq + qi * pl.q_bytes, &q_map, 0, (int)p.row0, 0, 0, &bar.q_full[qi]);
       }
       __syncwarp();
-      for (int t = p.t0; t < p.t1 && ok; ++t) {
-        // this lane's box: rows [64 t + lane box_rows, ..) of the sequence; zeros where there
-        // is no such page
-        int page = sh.num_pages, row = 0;
-        const int pos = t * kTcTile + lane * pl.box_rows;
-        if (lane < pl.groups && pos < p.len) {
-          const int id = __ldg(page_table + (long long)p.n * sh.max_pages + pos / sh.page_size);
-          row = pos % sh.page_size;
-          if (id >= 0 && id < sh.num_pages) page = id;
-        }
-        if (rope) {
-          const uint32_t r = rt % pl.rope_slots, use = rt / pl.rope_slots;
-          ++rt;
-          if (use > 0) ok = mbar_wait(&bar.rope_empty[r], (use - 1) & 1, kWaitLimit);
-          if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-          if (lane == 0) mbar_arrive_expect_tx(&bar.rope_full[r], kChunk);
-          __syncwarp();
-          if (lane < pl.groups)
-            tma_load_3d(srope + r * kChunk + lane * pl.box_rows * 128, &c_map, sh.rank, row, page,
-                        &bar.rope_full[r]);
-        }
-        for (int j = 0; j < npair; ++j) {
-          if (slot_use > 0) ok = mbar_wait(&bar.empty[slot], (slot_use - 1) & 1, kWaitLimit);
-          if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-          if (lane == 0) mbar_arrive_expect_tx(&bar.full[slot], kSlot);
-          __syncwarp();
-          if (lane < pl.groups) {
-            uint8_t* d = sslot + slot * kSlot + lane * pl.box_rows * 128;
-            tma_load_3d(d, &c_map, 128 * j, row, page, &bar.full[slot]);
-            tma_load_3d(d + kChunk, &c_map, 128 * j + 64, row, page, &bar.full[slot]);
-          }
-          if (++slot == (uint32_t)pl.slots) {
-            slot = 0;
-            ++slot_use;
-          }
-        }
+      if (++qi == (uint32_t)pl.nq) {
+        qi = 0;
+        ++quse;
       }
     }
-    if (!ok) {
-      // let the copies in flight land before the memory goes away
-      for (uint32_t i = 0; i < (uint32_t)pl.slots; ++i) {
-        const uint32_t uses = slot_use + (i < slot ? 1 : 0);
-        if (uses) mbar_wait(&bar.full[i], (uses - 1) & 1, kWaitLimit);
-      }
-      for (uint32_t r = 0; r < (uint32_t)pl.rope_slots; ++r) {
-        const uint32_t uses = rt / pl.rope_slots + (r < rt % pl.rope_slots ? 1 : 0);
-        if (uses > 1) mbar_wait(&bar.rope_full[r], (uses - 2) & 1, kWaitLimit);
-      }
-      for (uint32_t i = 0; i < (uint32_t)pl.nq; ++i) {
-        const uint32_t uses = it / pl.nq + (i < it % pl.nq ? 1 : 0);
-        if (uses > 1) mbar_wait(&bar.q_full[i], (uses - 2) & 1, kWaitLimit);
-      }
+    for (uint32_t i = 0; !ok && i < (uint32_t)pl.nq; ++i) {
+      const uint32_t uses = quse + (i < qi ? 1 : 0);
+      if (uses) mbar_wait(&bar.q_full[i], (uses - 1) & 1, kDrainLimit);
     }
-  } else if (warp == 1 && lane == 0) {
+  } else if (warp == 1) {
     // ------------------------------------------------------------- the MMAs
+    // The whole warp runs the loop, one lane issues (see elect_one).
     const uint32_t id_qk = idesc_bf16(128, kTcTile, false, false);
     const uint32_t id_pv = idesc_bf16(128, nr, true, false);
-    const uint32_t aslot = smem_u32(sslot), arope = smem_u32(srope), ap = smem_u32(sp);
+    // first descriptors; a K step is 32 bytes further in a K-major block, 2048 in V
+    const uint64_t dq = desc_kmajor_sw128(smem_u32(sq), nr, 0);
+    const uint64_t dk = desc_kmajor_sw128(smem_u32(sst), kTcTile, 0);
+    const uint64_t dr = desc_kmajor_sw128(smem_u32(srope), kTcTile, 0);
+    const uint64_t dv = desc_mnmajor_sw128(smem_u32(sst), kTcTile, 0);
+    const uint64_t dp = desc_kmajor_sw128(smem_u32(sp), nr, 0);
+    const uint32_t block = (uint32_t)(nr * 8);            // 64 columns of Q, in 16 bytes
     LatentWalk walk(st);
     LatentPiece p;
-    uint32_t it = 0, g = 0, rt = 0;                      // blocks, tiles, rope slots
-    uint32_t slot = 0, use = 0;                          // of the next scores' pair
-    uint32_t vslot = 0;                                  // of the next values' pair
-    // next pair (or, with k = -1, the rope columns) of the scores of tile `t`
-    auto issue_qk = [&](int k, uint32_t t, uint32_t aq) {
+    uint32_t it = 0, g = 0;                              // blocks, tiles
+    uint32_t rs = 0, stage = 0, use = 0;                 // of the next scores
+    uint32_t vstage = 0;                                 // of the next values
+    uint32_t qi = 0, quse = 0;
+    // stage s of the scores of tile `t` (it is there)
+    auto issue_qk = [&](int s, uint32_t t, uint64_t q0) {
       const uint32_t d = tb + kTmemS + (t & 1) * kTcTile;
-      if (k < 0) {
-        const uint32_t r = rt % pl.rope_slots;
-        const uint32_t a = aq + (uint32_t)(2 * npair * nr * 128), b = arope + r * kChunk;
+      const uint64_t a = q0 + (uint64_t)(2 * s * pl.spair * block);
+      const uint64_t b = dk + (uint64_t)(stage * (stage_bytes / 16));
+      const uint64_t ra = q0 + (uint64_t)(2 * npair * block), rb = dr + (uint64_t)(rs * (kChunk / 16));
+      const bool two = s * pl.spair + 1 < npair && pl.spair == 2;
+      if (elect_one()) {
+        if (rope && s == 0) {
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          mma_ss(d, desc_kmajor_sw128(a, nr, kk), desc_kmajor_sw128(b, kTcTile, kk), id_qk, kk > 0);
-        mma_commit(&bar.rope_empty[r]);
-        ++rt;
-        return;
+          for (int kk = 0; kk < 4; ++kk) mma_ss_all(d, ra + 2 * kk, rb + 2 * kk, id_qk, kk > 0);
+          mma_commit(&bar.rope_empty[rs]);
+        }
+        mma_ss_all(d, a, b, id_qk, rope || s > 0);
+#pragma unroll
+        for (int kk = 1; kk < 8; ++kk)
+          mma_ss_all(d, a + (kk >> 2) * block + 2 * (kk & 3), b + (kk >> 2) * (kChunk / 16) + 2 * (kk & 3),
+                     id_qk, 1);
+        if (two) {
+#pragma unroll
+          for (int kk = 8; kk < 16; ++kk)
+            mma_ss_all(d, a + (kk >> 2) * block + 2 * (kk & 3),
+                       b + (kk >> 2) * (kChunk / 16) + 2 * (kk & 3), id_qk, 1);
+        }
+        if (s == pl.ns - 1) mma_commit(&bar.s_full[t & 1]);
       }
-      const uint32_t a = aq + (uint32_t)(2 * k * nr * 128), b = aslot + slot * kSlot;
-#pragma unroll
-      for (int kk = 0; kk < 8; ++kk)
-        mma_ss(d, desc_kmajor_sw128(a, nr, kk), desc_kmajor_sw128(b, kTcTile, kk), id_qk,
-               rope || k > 0 || kk > 0);
-      if (++slot == (uint32_t)pl.slots) {
-        slot = 0;
+      __syncwarp();
+      if (rope && s == 0 && ++rs == (uint32_t)pl.rope_slots) rs = 0;
+      if (++stage == (uint32_t)pl.stages) {
+        stage = 0;
         ++use;
       }
     };
-    auto qk_bar = [&](int k) -> uint64_t* { return k < 0 ? &bar.rope_full[rt % pl.rope_slots] : &bar.full[slot]; };
-    auto qk_par = [&](int k) -> uint32_t { return (k < 0 ? rt / pl.rope_slots : use) & 1; };
 
     while (ok && walk.next(sh, seq_lens, cu_seqlens, nr, kTcTile, &p)) {
-      const uint32_t qi = it % pl.nq;
-      const uint32_t aq = smem_u32(sq + qi * pl.q_bytes);
+      const uint64_t q0 = dq + (uint64_t)(qi * (pl.q_bytes / 16));
       const int nt = p.t1 - p.t0;
-      ok = mbar_wait(&bar.q_full[qi], (it / pl.nq) & 1, kWaitLimit);
-      const int k0 = rope ? -1 : 0;
-      int k = k0;                                        // next part of the scores of tile i
+      ok = __all_sync(kAll, mbar_wait(&bar.q_full[qi], quse & 1, kWaitLimit));
+      int s = 0;                                         // next stage of the scores of tile i
       for (int i = 0; i <= nt && ok; ++i) {
-        // scores of tile i (g + 1 for i > 0) and, between them, the values of tile i - 1
+        // scores of tile i (g + 1 for i > 0) and, between them, the values of tile i - 1.  Their
+        // place was read by the softmax of the tile before last, whose weights have been used.
         const uint32_t ts = i == 0 ? g : g + 1;
         const bool scores = i < nt;
-        if (scores && ts >= 2) ok = ok && mbar_wait(&bar.s_empty[ts & 1], ((ts >> 1) - 1) & 1, kWaitLimit);
         if (i > 0) {
-          const uint32_t pb = g % pl.np;
+          const uint32_t pb = pl.np == 2 ? g & 1 : 0, ppar = (pl.np == 2 ? g >> 1 : g) & 1;
           uint32_t polls = 0;
-          while (ok && !mbar_test_wait(&bar.p_full[pb], (g / pl.np) & 1)) {
-            if (scores && k < npair && mbar_test_wait(qk_bar(k), qk_par(k))) {
-              tc_fence_after();
-              issue_qk(k++, ts, aq);
-              if (k == npair) mma_commit(&bar.s_full[ts & 1]);
-            }
+          while (ok && !__all_sync(kAll, mbar_test_wait(&bar.p_full[pb], ppar))) {
+            if (scores && s < pl.ns && __all_sync(kAll, mbar_test_wait(&bar.full[stage], use & 1)))
+              issue_qk(s++, ts, q0);
             if (++polls > kPollLimit) ok = false;
           }
-          if (i == 1 && it > 0)                          // the block before has left O^T
-            ok = ok && mbar_wait(&bar.o_empty, (it - 1) & 1, kWaitLimit);
+          if (ok && i == 1 && it > 0)                    // the block before has left O^T
+            ok = __all_sync(kAll, mbar_wait(&bar.o_empty, (it - 1) & 1, kWaitLimit));
           if (!ok) break;
           tc_fence_after();
-          for (int j = 0; j < npair; ++j) {
-            const uint32_t a = aslot + vslot * kSlot, b = ap + pb * pl.p_bytes;
+          const uint64_t b = dp + (uint64_t)(pb * (pl.p_bytes / 16));
+          for (int v = 0; v < pl.ns; ++v) {
+            const uint64_t a = dv + (uint64_t)(vstage * (stage_bytes / 16));
+            const uint32_t d = tb + v * pl.spair * nr;
+            const bool two = v * pl.spair + 1 < npair && pl.spair == 2;
+            if (elect_one()) {
+              mma_ss_all(d, a, b, id_pv, i > 1);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_ss(tb + j * nr, desc_mnmajor_sw128(a, kTcTile, kk), desc_kmajor_sw128(b, nr, kk),
-                     id_pv, i > 1 || kk > 0);
-            mma_commit(&bar.empty[vslot]);
-            if (++vslot == (uint32_t)pl.slots) vslot = 0;
+              for (int kk = 1; kk < 4; ++kk) mma_ss_all(d, a + 128 * kk, b + 2 * kk, id_pv, 1);
+              if (two) {
+                mma_ss_all(d + nr, a + kPair / 16, b, id_pv, i > 1);
+#pragma unroll
+                for (int kk = 1; kk < 4; ++kk)
+                  mma_ss_all(d + nr, a + kPair / 16 + 128 * kk, b + 2 * kk, id_pv, 1);
+              }
+              mma_commit(&bar.empty[vstage]);
+              if (v == pl.ns - 1) mma_commit(&bar.pv_done[pb]);
+            }
+            __syncwarp();
+            if (++vstage == (uint32_t)pl.stages) vstage = 0;
           }
-          mma_commit(&bar.pv_done[pb]);
           ++g;
         }
         if (scores) {
-          while (ok && k < npair) {
-            ok = mbar_wait(qk_bar(k), qk_par(k), kWaitLimit);
-            if (!ok) break;
-            tc_fence_after();
-            issue_qk(k++, ts, aq);
-            if (k == npair) mma_commit(&bar.s_full[ts & 1]);
+          while (ok && s < pl.ns) {
+            ok = __all_sync(kAll, mbar_wait(&bar.full[stage], use & 1, kWaitLimit));
+            if (ok) issue_qk(s++, ts, q0);
           }
-          k = k0;
-          if (i == nt - 1) mma_commit(&bar.q_empty[qi]);
+          s = 0;
+          if (i == nt - 1) {
+            if (elect_one()) mma_commit(&bar.q_empty[qi]);
+            __syncwarp();
+          }
         }
       }
       ++it;
+      if (++qi == (uint32_t)pl.nq) {
+        qi = 0;
+        ++quse;
+      }
     }
     if (!ok) {
-      mma_commit(&bar.drain);
+      if (elect_one()) mma_commit(&bar.drain);
+      __syncwarp();
       mbar_wait(&bar.drain, 0, kWaitLimit);
     }
-  } else if (warp >= 4) {
+  } else {
     // ------------------------------------------------------------- softmax and results
-    const int wq = warp - 4, r = 32 * wq + lane, t128 = tid - 128;
+    const int wq = warp & 3, half = (warp - 4) >> 2, r = 32 * wq + lane, ts = tid - 128;
     const uint32_t tl = tb + ((uint32_t)(32 * wq) << 16);
     const bool has_rows = 32 * wq < nr;
     const float c = sh.scale * kLog2e;
     LatentWalk walk(st);
     LatentPiece p;
-    uint32_t g = 0;
+    uint32_t g = 0, pb = 0, puse = 0;                    // tiles; next P buffer
     bool dead = false;
+    // PV of the tile `back` tiles ago is done
+    auto pv_wait = [&](uint32_t back) {
+      const uint32_t t = g - back;
+      return mbar_wait(&bar.pv_done[pl.np == 2 ? t & 1 : 0], (pl.np == 2 ? t >> 1 : t) & 1, kWaitLimit);
+    };
     while (!dead && walk.next(sh, seq_lens, cu_seqlens, nr, kTcTile, &p)) {
       const bool row = r < p.rows;
       const int lim = min(p.start + (p.row_in_seq + r) / sh.H + 1, p.len);
@@ -342,109 +398,117 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
       for (int t = p.t0; t < p.t1; ++t, ++g) {
         ok = ok && mbar_wait(&bar.s_full[g & 1], (g >> 1) & 1, kWaitLimit);
         tc_fence_after();
-        const int k0 = t * kTcTile;
-        const bool mixed = k0 + kTcTile > low;
-        uint32_t s[4][16];
-        if (has_rows) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) tmem_ld16(tl + kTmemS + (g & 1) * kTcTile + 16 * i, s[i]);
-          tmem_wait_ld();
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.s_empty[g & 1]);
+        const int k0 = t * kTcTile + 32 * half;
+        const bool mixed = (t + 1) * kTcTile > low;
+        uint32_t s[2][16];
         bool need = false;
         float mt = -INFINITY;
         if (has_rows) {
+          tmem_ld16(tl + kTmemS + (g & 1) * kTcTile + 32 * half, s[0]);
+          tmem_ld16(tl + kTmemS + (g & 1) * kTcTile + 32 * half + 16, s[1]);
+          tmem_wait_ld();
           if (mixed) {
 #pragma unroll
-            for (int i = 0; i < 64; ++i)
+            for (int i = 0; i < 32; ++i)
               if (k0 + i >= lim) s[i >> 4][i & 15] = 0xff800000u;      // -inf
           }
 #pragma unroll
-          for (int i = 0; i < 64; ++i) mt = fmaxf(mt, __uint_as_float(s[i >> 4][i & 15]));
-          mt = fmaxf(m, mt * c);                         // c > 0: the scaled maximum
-          need = row && m != -INFINITY && mt > m + 8.f;
-          if (m == -INFINITY) m = mt;
+          for (int i = 0; i < 32; ++i) mt = fmaxf(mt, __uint_as_float(s[i >> 4][i & 15]));
+          mt *= c;                                       // c > 0: the scaled maximum
+          need = row && mt > (m == -INFINITY ? m : m + 8.f);
+          if (r < nr) s_half[half][r] = mt;
         }
+        tc_fence_before();
         // rows that some query row does not see: nothing that 0 * would turn into a NaN
         if (mixed) {
-          const int first = max(low - k0, 0), per = sh.rank / 8;
-          for (int i = t128; i < (kTcTile - first) * per; i += 128) {
-            const int tok = first + i / per, c8 = i % per;
-            const uint32_t sl = (g * npair + (c8 >> 4)) % pl.slots;
-            uint4* w = reinterpret_cast<uint4*>(sslot + sl * kSlot + ((c8 >> 3) & 1) * kChunk +
-                                                tok * 128 + (c8 & 7) * 16);
+          const int first = max(low - t * kTcTile, 0), per = sh.rank / 8;
+          for (int i = ts; i < (kTcTile - first) * per; i += kSoft) {
+            const int tok = first + i / per, c8 = i % per, pair = c8 >> 4;
+            const uint32_t sg = (g * pl.ns + pair / pl.spair) % pl.stages;
+            uint4* w = reinterpret_cast<uint4*>(sst + sg * stage_bytes + (pair % pl.spair) * kPair +
+                                                ((c8 >> 3) & 1) * kChunk + tok * 128 +
+                                                (((c8 & 7) ^ (tok & 7)) << 4));
             const uint4 a = *w;
             const uint4 b = make_uint4(zero_bad(a.x), zero_bad(a.y), zero_bad(a.z), zero_bad(a.w));
             if (a.x != b.x || a.y != b.y || a.z != b.z || a.w != b.w) *w = b;
           }
         }
-        if (named_bar_or(1, 128, need || !ok)) {
-          if (named_bar_or(1, 128, !ok)) { dead = true; break; }
-          // rescale O^T to the maxima of now (tiles before this one have been added)
+        if (named_bar_or(1, kSoft, need || !ok)) {
+          // the first tile, or a maximum that passed: O^T and sums go to the maxima of now
           float al = 1.f;
-          if (has_rows && row && m != -INFINITY) {
-            al = ex2(m - mt);
+          if (has_rows && row) {
+            const float mn = fmaxf(m, fmaxf(s_half[0][r], s_half[1][r]));
+            if (m != -INFINITY) al = ex2(m - mn);
             l *= al;
-            m = mt;
+            m = mn;
           }
-          if (r < nr) s_row[r] = al;
-          ok = ok && mbar_wait(&bar.pv_done[(g - 1) % pl.np], ((g - 1) / pl.np) & 1, kWaitLimit);
-          named_bar(1, 128);
-          tc_fence_after();
-          for (int j = 0; j < npair; ++j)
-            for (int i = 0; i < nr; i += 16) {
-              uint32_t o[16];
-              tmem_ld16(tl + j * nr + i, o);
-              tmem_wait_ld();
+          if (half == 0 && r < nr) s_row[r] = al;
+          if (t > p.t0) ok = ok && pv_wait(1);           // the tiles before have been added
+          if (named_bar_or(1, kSoft, !ok)) { dead = true; break; }
+          if (t > p.t0) {
+            tc_fence_after();
+            for (int j = half; j < npair; j += 2)
+              for (int i = 0; i < nr; i += 16) {
+                uint32_t o[16];
+                tmem_ld16(tl + j * nr + i, o);
+                tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * s_row[i + e]);
-              tmem_st16(tl + j * nr + i, o);
-            }
-          tmem_wait_st();
-          tc_fence_before();
+                for (int e = 0; e < 16; ++e)
+                  o[e] = __float_as_uint(__uint_as_float(o[e]) * s_row[i + e]);
+                tmem_st16(tl + j * nr + i, o);
+              }
+            tmem_wait_st();
+            tc_fence_before();
+          }
         }
         if (has_rows) {
           const float ms = m == -INFINITY ? 0.f : m;
-          if (g >= (uint32_t)pl.np)
-            ok = ok && mbar_wait(&bar.pv_done[g % pl.np], (g / pl.np - 1) & 1, kWaitLimit);
-          uint8_t* const pr = sp + (g % pl.np) * pl.p_bytes + r * 128;
+          if (puse > 0) ok = ok && pv_wait(pl.np);       // the buffer's last values are done
+          uint8_t* const pr = sp + pb * pl.p_bytes + r * 128;
+          float l0 = 0.f, l1 = 0.f;
 #pragma unroll
-          for (int c8 = 0; c8 < 8; ++c8) {
+          for (int c8 = 0; c8 < 4; ++c8) {
             float e[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < 8; ++i)
               e[i] = row ? ex2(fmaf(__uint_as_float(s[c8 >> 1][8 * (c8 & 1) + i]), c, -ms)) : 0.f;
-              l += e[i];
-            }
+            l0 += (e[0] + e[1]) + (e[2] + e[3]);
+            l1 += (e[4] + e[5]) + (e[6] + e[7]);
             if (r < nr)
-              *reinterpret_cast<uint4*>(pr + ((c8 ^ (r & 7)) << 4)) =
+              *reinterpret_cast<uint4*>(pr + (((4 * half + c8) ^ (r & 7)) << 4)) =
                   make_uint4(pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3]), pack_bf16(e[4], e[5]),
                              pack_bf16(e[6], e[7]));
           }
+          l += l0 + l1;
         }
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.p_full[g % pl.np]);
+        if (lane == 0) mbar_arrive(&bar.p_full[pb]);
+        if (++pb == (uint32_t)pl.np) {
+          pb = 0;
+          ++puse;
+        }
       }
       if (dead) break;
       // ---- results: whole blocks to the output, shared ones to a partial slot
       const bool first = p.t0 == 0, last = p.t1 == p.tiles;
       const int slot = first && last ? -1 : 2 * (int)blockIdx.x + (first ? 1 : 0);
-      if (r < nr) {
+      if (r < nr) s_half[half][r] = l;
+      ok = ok && pv_wait(1);
+      if (named_bar_or(1, kSoft, !ok)) break;
+      if (half == 0 && r < nr) {
+        l += s_half[1][r];
         s_row[r] = l == 0.f ? 0.f : 1.0f / l;
         const float z = l == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m) * kLn2 + logf(l);
         if (slot >= 0) pt.lse[slot * nr + r] = z;
         else if (lse && row) lse[p.row0 + r] = z;
       }
-      if (slot >= 0 && first && t128 == 0)
+      if (slot >= 0 && first && ts == 0)
         pt.head[blockIdx.x] =
             make_int4((int)p.row0, p.rows, latent_cta_of(p.pos + p.tiles - 1, st.W, st.G), 0);
-      ok = ok && mbar_wait(&bar.pv_done[(g - 1) % pl.np], ((g - 1) / pl.np) & 1, kWaitLimit);
-      if (named_bar_or(1, 128, !ok)) break;
+      named_bar(1, kSoft);
       tc_fence_after();
-      for (int j = 0; j < npair; ++j) {
+      for (int j = half; j < npair; j += 2) {
         const int d = 128 * j + r;
         for (int i = 0; i < p.rows; i += 16) {
           uint32_t o[16];
@@ -466,7 +530,7 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
         }
       }
       tc_fence_before();
-      named_bar(1, 128);                                 // s_row is free again
+      named_bar(1, kSoft);                               // s_row and s_half are free again
       if (lane == 0) mbar_arrive(&bar.o_empty);
     }
   }
@@ -513,14 +577,18 @@ cudaError_t launch_latent_tc(const void* q, const void* cache, const int32_t* pa
   const LatentPartials pt = latent_partials(buf, G, nr);
   const uint64_t D = sh.rank + sh.rope;
   const uint64_t rows = (uint64_t)(sh.L > 0 ? (long long)sh.N * sh.L : sh.T) * sh.H;
-  CUtensorMap q_map, c_map;
-  if (!make_row_map_3d(&q_map, q, D, rows, 1, D * 2, D * 2, 64, (uint32_t)nr) ||
-      !make_row_map_3d(&c_map, cache, D, sh.page_size, sh.num_pages, sh.row_stride * 2,
-                       sh.page_stride * 2, 64, (uint32_t)pl.box_rows))
+  CUtensorMap q_map, c_map, r_map;
+  const auto cache_map = [&](CUtensorMap* m, uint32_t chunks) {
+    return make_chunk_map_4d(m, cache, sh.page_size, D / 64, sh.num_pages, sh.row_stride * 2,
+                             sh.page_stride * 2, (uint32_t)pl.box_rows, chunks);
+  };
+  if (!make_chunk_map_4d(&q_map, q, rows, D / 64, 1, D * 2, D * 2, (uint32_t)nr,
+                         (uint32_t)(D / 64)) ||
+      !cache_map(&c_map, 2) || !cache_map(&r_map, 1))
     return cudaErrorInvalidValue;
   KDA_TIMED(KDA_KERNEL_LATENT_ATTN, stream,
             kda_latent_tc_kernel<<<G, kTcThreads, kTcSmem + 1024, stream>>>(
-                q_map, c_map, page_table, seq_lens, cu_seqlens, static_cast<bf16*>(out), lse, sh,
+                q_map, c_map, r_map, page_table, seq_lens, cu_seqlens, static_cast<bf16*>(out), lse, sh,
                 pl, pt));
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;

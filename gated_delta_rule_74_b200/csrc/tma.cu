@@ -29,14 +29,14 @@ EncodeTiled encoder() {
 
 }  // namespace
 
-static bool encode_3d(CUtensorMap* map, bool fp32, const void* base, uint64_t d0, uint64_t d1,
+bool make_tile_map_3d(CUtensorMap* map, bool fp32, const void* base, uint64_t d0, uint64_t d1,
                       uint64_t d2, uint64_t stride1, uint64_t stride2, uint32_t box0,
-                      uint32_t box1, uint32_t box2, bool swizzle128) {
+                      uint32_t box2, bool swizzle128) {
   const EncodeTiled enc = encoder();
   if (!enc || !base) return false;
   const cuuint64_t dims[3] = {d0, d1, d2};
   const cuuint64_t strides[2] = {stride1, stride2};
-  const cuuint32_t box[3] = {box0, box1, box2};
+  const cuuint32_t box[3] = {box0, 1u, box2};
   const cuuint32_t elem[3] = {1u, 1u, 1u};
   const CUresult r =
       enc(map, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
@@ -46,15 +46,20 @@ static bool encode_3d(CUtensorMap* map, bool fp32, const void* base, uint64_t d0
   return r == CUDA_SUCCESS;
 }
 
-bool make_tile_map_3d(CUtensorMap* map, bool fp32, const void* base, uint64_t d0, uint64_t d1,
-                      uint64_t d2, uint64_t stride1, uint64_t stride2, uint32_t box0,
-                      uint32_t box2, bool swizzle128) {
-  return encode_3d(map, fp32, base, d0, d1, d2, stride1, stride2, box0, 1u, box2, swizzle128);
-}
-
-bool make_row_map_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
-                     uint64_t stride1, uint64_t stride2, uint32_t box0, uint32_t box1) {
-  return encode_3d(map, false, base, d0, d1, d2, stride1, stride2, box0, box1, 1u, true);
+bool make_chunk_map_4d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t chunks,
+                       uint64_t outer, uint64_t row_stride, uint64_t outer_stride,
+                       uint32_t box_rows, uint32_t box_chunks) {
+  const EncodeTiled enc = encoder();
+  if (!enc || !base) return false;
+  const cuuint64_t dims[4] = {64, rows, chunks, outer};
+  const cuuint64_t strides[3] = {row_stride, 128, outer_stride};
+  const cuuint32_t box[4] = {64u, box_rows, box_chunks, 1u};
+  const cuuint32_t elem[4] = {1u, 1u, 1u, 1u};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims,
+                         strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
 }
 
 }  // namespace kda

@@ -19,8 +19,11 @@ bool make_tile_map_3d(CUtensorMap* map, bool fp32, const void* base, uint64_t d0
                       uint64_t d2, uint64_t stride1, uint64_t stride2, uint32_t box0,
                       uint32_t box2, bool swizzle128);
 
-// The same with boxes of box0 x box1 x 1 elements: runs of d1 rows (128-byte swizzle, bf16).
-bool make_row_map_3d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
-                     uint64_t stride1, uint64_t stride2, uint32_t box0, uint32_t box1);
+// A 4-D bf16 map that brings `box_rows` rows of `box_chunks` 64-column chunks in one box,
+// chunk after chunk, each [box_rows][128 B] with the 128-byte swizzle (the K-major operand
+// layout).  The tensor: [outer][rows][64 * chunks] with row and outer strides in bytes.
+bool make_chunk_map_4d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t chunks,
+                       uint64_t outer, uint64_t row_stride, uint64_t outer_stride,
+                       uint32_t box_rows, uint32_t box_chunks);
 
 }  // namespace kda
