@@ -2,27 +2,30 @@
 //
 // For a block of up to 96 query rows (new token, head) and a tile of 64 cached rows C
 // [64][rank + rope], whose first `rank` columns are the values too:
-//     S (128 x 64)      = Q C^T                      Q's rows on the TMEM lanes
-//     P (rows x 64)     = 2^(scale log2e S - m)      to shared memory as bf16
-//     O^T (rank x rows) += C[:, 0:rank]^T P^T        the value columns on the lanes
+//     S^T (64 x rows)   = C Q^T                      tokens on the TMEM lanes
+//     P (64 x rows)     = 2^(scale log2e S - m)      to shared memory as bf16
+//     O^T (rank x rows) += C[:, 0:rank]^T P          the value columns on the lanes
 // with the running maximum m and sum of the softmax.  The tile is read from memory once and
 // serves both products from one place in shared memory: K-major for the scores, the same
-// bytes MN-major for the values.  O is held transposed because a row needs its 512 values
-// beside S in 512 TMEM columns: O^T takes `rows` columns for each 128 of them, so that 96
-// rows (all heads of a model at one token) fit with two score tiles; with Q's rows on the
-// lanes O alone would take all 512 columns.
+// bytes MN-major for the values.  Everything is held transposed.  O^T takes `rows` TMEM
+// columns for each 128 of its values, so that 96 rows (all heads of a model at one token) fit
+// beside the scores; with rows on the lanes, O alone would take all 512 columns.  S^T makes
+// the tile the M side of both products, so that few rows (12 heads) cost the MMAs few
+// operand bytes: 2.5 KB of shared memory an MMA of 64 x 16 against 6 KB of 128 x 64 (rows
+// padded to the lanes), which held the decode step at 65% of the memory's rate.
 //
 // Bound by the cache's bytes for few rows (12 heads: 24 FLOP a byte), near the balance of
-// memory and tensor cores at 96 rows.  The MMAs stage A and B in shared memory; at N = 64
-// reading them takes 48 of the 128-byte cycles that the 32 of the product would leave.
+// memory and tensor cores at 96 rows.
 //
 // One CTA an SM, its stretch of tiles as latent_attn.cuh lays it out.  Warps 0 and 2 bring
 // the tiles by TMA into a ring of stages (256 columns x 64 rows; the rope columns apart), one
 // box a run of rows inside of a page, warp 3 Q; warp 1 issues the MMAs; warps 4..11 do the
-// softmax (thread = row, two warps a lane quarter with half of the columns each), the rare
-// rescaling of O^T and the results (thread = value column).  The maximum that the weights
-// refer to moves only when a row's passes it by 2^8, so that O^T is rescaled a few times a
-// sequence; the weights stay below 2^8, far inside of bf16 and fp32.
+// softmax (two warps a lane quarter of 16 tokens, half of the rows each; a thread holds two
+// tokens and two of every eight rows), the rare rescaling of O^T and the results (thread =
+// value column).  The maximum that the weights refer to moves only when a score passes it
+// by 2^8: a tile then needs one vote, no reduction over the tokens, O^T is rescaled a few
+// times a sequence, and the weights stay below 2^8, far inside of bf16 and fp32.  Sums are
+// kept by thread and joined at the end of a block.
 // The scores of tile t + 1 are issued while tile t's softmax runs, as far as stages allow
 // (all of them up to 64 rows, half of the columns at 96); whichever of "the next stage is
 // there" and "the weights are there" comes first goes first.  A wait between MMAs costs
@@ -52,10 +55,11 @@ constexpr int kTcMaxRows = 96;
 constexpr uint32_t kChunk = 64 * 128;              // 64 cached rows x 64 columns
 constexpr uint32_t kPair = 2 * kChunk;
 constexpr int kMaxStages = 8;
-constexpr uint32_t kTcSmem = 229376;               // Q, stages, P; + 1024 for the alignment
-constexpr uint32_t kTmemCols = 512, kTmemS = 384;
+constexpr uint32_t kTcSmem = 229376;               // Q, stages, P
+constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kWaitLimit = 1u << 22, kPollLimit = 1u << 26, kDrainLimit = 1u << 14;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kNone = -1e30f;                    // maximum of a row that has seen nothing
 
 // How shared memory is divided, from the block's rows and the row's columns.
 struct TcPlan {
@@ -95,7 +99,7 @@ struct TcBars {
   uint64_t q_full[2], q_empty[2];
   uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t rope_empty[2];
-  uint64_t s_full[2];
+  uint64_t s_full[2], s_empty;
   uint64_t p_full[2], pv_done[2];
   uint64_t o_empty, drain;
 };
@@ -111,6 +115,8 @@ __device__ __forceinline__ uint32_t zero_bad(uint32_t w) {     // two bf16: inf,
   return w;
 }
 
+// TMEM: O^T, rank / 128 blocks of NR columns, then two buffers of S^T, or one at 96 rows.
+template <int NR>
 __global__ void __launch_bounds__(kTcThreads, 1)
 kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                      const __grid_constant__ CUtensorMap c_map,
@@ -119,17 +125,22 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                      const int32_t* __restrict__ seq_lens,
                      const int32_t* __restrict__ cu_seqlens, bf16* __restrict__ out,
                      float* __restrict__ lse, LatentAttnShape sh, TcPlan pl, LatentPartials pt) {
-  extern __shared__ uint8_t smem_raw[];
+  // the alignment is part of the declaration: there is no room to round up (a block of 96 rows
+  // fills the 227 KB, 3 KB of them the variables below)
+  extern __shared__ __align__(1024) uint8_t sm[];
   __shared__ TcBars bar;
   __shared__ LatentStart st;
   __shared__ long long s_sum[33];
-  __shared__ float s_row[kTcMaxRows];               // rescaling factors, then 1 / sum
-  __shared__ float s_half[2][kTcMaxRows];           // the column halves' maxima, then sums
+  __shared__ float2 s_m2[NR / 2];                   // maxima the weights refer to, scaled
+  __shared__ uint8_t s_more[NR];                    // tokens each row sees more than the first
+  __shared__ float s_row[NR];                       // rescaling factors, then 1 / sum
+  __shared__ float s_red[4][NR];                    // the lane quarters' maxima, then sums
   __shared__ uint32_t s_tmem;
-  uint8_t* const sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                                 ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int nr = pl.nr, npair = pl.npair;
+  constexpr int nr = NR, kSBuf = NR <= 80 ? 2 : 1;
+  constexpr uint32_t kTmemS = 4 * NR;
+  const int npair = pl.npair;
+  float* const s_m = reinterpret_cast<float*>(s_m2);
   const uint32_t stage_bytes = pl.spair * kPair;
   uint8_t* const sq = sm;
   uint8_t* const sst = sq + pl.nq * pl.q_bytes;
@@ -153,6 +164,7 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
       mbar_init(&bar.full[i], 2);                   // warps 0 and 2
       mbar_init(&bar.empty[i], 1);
     }
+    mbar_init(&bar.s_empty, kSoft / 32);
     mbar_init(&bar.o_empty, kSoft / 32);
     mbar_init(&bar.drain, 1);
     fence_mbar_init();
@@ -258,14 +270,14 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
   } else if (warp == 1) {
     // ------------------------------------------------------------- the MMAs
     // The whole warp runs the loop, one lane issues (see elect_one).
-    const uint32_t id_qk = idesc_bf16(128, kTcTile, false, false);
-    const uint32_t id_pv = idesc_bf16(128, nr, true, false);
-    // first descriptors; a K step is 32 bytes further in a K-major block, 2048 in V
+    const uint32_t id_qk = idesc_bf16(kTcTile, nr, false, false);
+    const uint32_t id_pv = idesc_bf16(128, nr, true, true);
+    // first descriptors; a K step is 32 bytes further in a K-major block, 2048 in V, 512 in P
     const uint64_t dq = desc_kmajor_sw128(smem_u32(sq), nr, 0);
     const uint64_t dk = desc_kmajor_sw128(smem_u32(sst), kTcTile, 0);
     const uint64_t dr = desc_kmajor_sw128(smem_u32(srope), kTcTile, 0);
     const uint64_t dv = desc_mnmajor_sw128(smem_u32(sst), kTcTile, 0);
-    const uint64_t dp = desc_kmajor_sw128(smem_u32(sp), nr, 0);
+    const uint64_t dp = desc_mnmajor_sw32(smem_u32(sp), kTcTile, 0);
     const uint32_t block = (uint32_t)(nr * 8);            // 64 columns of Q, in 16 bytes
     LatentWalk walk(st);
     LatentPiece p;
@@ -275,7 +287,7 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
     uint32_t qi = 0, quse = 0;
     // stage s of the scores of tile `t` (it is there)
     auto issue_qk = [&](int s, uint32_t t, uint64_t q0) {
-      const uint32_t d = tb + kTmemS + (t & 1) * kTcTile;
+      const uint32_t d = tb + kTmemS + (kSBuf == 2 ? t & 1 : 0) * nr;
       const uint64_t a = q0 + (uint64_t)(2 * s * pl.spair * block);
       const uint64_t b = dk + (uint64_t)(stage * (stage_bytes / 16));
       const uint64_t ra = q0 + (uint64_t)(2 * npair * block), rb = dr + (uint64_t)(rs * (kChunk / 16));
@@ -283,21 +295,21 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
       if (elect_one()) {
         if (rope && s == 0) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) mma_ss_all(d, ra + 2 * kk, rb + 2 * kk, id_qk, kk > 0);
+          for (int kk = 0; kk < 4; ++kk) mma_ss_all(d, rb + 2 * kk, ra + 2 * kk, id_qk, kk > 0);
           mma_commit(&bar.rope_empty[rs]);
         }
-        mma_ss_all(d, a, b, id_qk, rope || s > 0);
+        mma_ss_all(d, b, a, id_qk, rope || s > 0);
 #pragma unroll
         for (int kk = 1; kk < 8; ++kk)
-          mma_ss_all(d, a + (kk >> 2) * block + 2 * (kk & 3), b + (kk >> 2) * (kChunk / 16) + 2 * (kk & 3),
+          mma_ss_all(d, b + (kk >> 2) * (kChunk / 16) + 2 * (kk & 3), a + (kk >> 2) * block + 2 * (kk & 3),
                      id_qk, 1);
         if (two) {
 #pragma unroll
           for (int kk = 8; kk < 16; ++kk)
-            mma_ss_all(d, a + (kk >> 2) * block + 2 * (kk & 3),
-                       b + (kk >> 2) * (kChunk / 16) + 2 * (kk & 3), id_qk, 1);
+            mma_ss_all(d, b + (kk >> 2) * (kChunk / 16) + 2 * (kk & 3),
+                       a + (kk >> 2) * block + 2 * (kk & 3), id_qk, 1);
         }
-        if (s == pl.ns - 1) mma_commit(&bar.s_full[t & 1]);
+        if (s == pl.ns - 1) mma_commit(&bar.s_full[kSBuf == 2 ? t & 1 : 0]);
       }
       __syncwarp();
       if (rope && s == 0 && ++rs == (uint32_t)pl.rope_slots) rs = 0;
@@ -307,21 +319,29 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
       }
     };
 
+    auto s_free = [&](uint32_t t) {                      // one buffer: tile t - 1 has been read
+      const bool f = t == 0 || __all_sync(kAll, mbar_test_wait(&bar.s_empty, (t - 1) & 1));
+      if (f) tc_fence_after();
+      return f;
+    };
+
     while (ok && walk.next(sh, seq_lens, cu_seqlens, nr, kTcTile, &p)) {
       const uint64_t q0 = dq + (uint64_t)(qi * (pl.q_bytes / 16));
       const int nt = p.t1 - p.t0;
       ok = __all_sync(kAll, mbar_wait(&bar.q_full[qi], quse & 1, kWaitLimit));
       int s = 0;                                         // next stage of the scores of tile i
       for (int i = 0; i <= nt && ok; ++i) {
-        // scores of tile i (g + 1 for i > 0) and, between them, the values of tile i - 1.  Their
-        // place was read by the softmax of the tile before last, whose weights have been used.
+        // scores of tile i (g + 1 for i > 0) and, between them, the values of tile i - 1.  With two
+        // score buffers their place was read by the softmax of the tile before last, whose
+        // weights have been used; with one, by the last tile's (s_empty).
         const uint32_t ts = i == 0 ? g : g + 1;
         const bool scores = i < nt;
         if (i > 0) {
           const uint32_t pb = pl.np == 2 ? g & 1 : 0, ppar = (pl.np == 2 ? g >> 1 : g) & 1;
           uint32_t polls = 0;
           while (ok && !__all_sync(kAll, mbar_test_wait(&bar.p_full[pb], ppar))) {
-            if (scores && s < pl.ns && __all_sync(kAll, mbar_test_wait(&bar.full[stage], use & 1)))
+            if (scores && s < pl.ns && (kSBuf == 2 || s > 0 || s_free(ts)) &&
+                __all_sync(kAll, mbar_test_wait(&bar.full[stage], use & 1)))
               issue_qk(s++, ts, q0);
             if (++polls > kPollLimit) ok = false;
           }
@@ -337,12 +357,12 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
             if (elect_one()) {
               mma_ss_all(d, a, b, id_pv, i > 1);
 #pragma unroll
-              for (int kk = 1; kk < 4; ++kk) mma_ss_all(d, a + 128 * kk, b + 2 * kk, id_pv, 1);
+              for (int kk = 1; kk < 4; ++kk) mma_ss_all(d, a + 128 * kk, b + 32 * kk, id_pv, 1);
               if (two) {
                 mma_ss_all(d + nr, a + kPair / 16, b, id_pv, i > 1);
 #pragma unroll
                 for (int kk = 1; kk < 4; ++kk)
-                  mma_ss_all(d + nr, a + kPair / 16 + 128 * kk, b + 2 * kk, id_pv, 1);
+                  mma_ss_all(d + nr, a + kPair / 16 + 128 * kk, b + 32 * kk, id_pv, 1);
               }
               mma_commit(&bar.empty[vstage]);
               if (v == pl.ns - 1) mma_commit(&bar.pv_done[pb]);
@@ -353,6 +373,10 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
           ++g;
         }
         if (scores) {
+          if (kSBuf == 1 && s == 0 && ts > 0) {
+            ok = __all_sync(kAll, mbar_wait(&bar.s_empty, (ts - 1) & 1, kWaitLimit));
+            tc_fence_after();
+          }
           while (ok && s < pl.ns) {
             ok = __all_sync(kAll, mbar_wait(&bar.full[stage], use & 1, kWaitLimit));
             if (ok) issue_qk(s++, ts, q0);
@@ -377,9 +401,12 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
     }
   } else {
     // ------------------------------------------------------------- softmax and results
-    const int wq = warp & 3, half = (warp - 4) >> 2, r = 32 * wq + lane, ts = tid - 128;
+    constexpr int kGroups = NR / 8;                      // of eight rows; half = 0 takes the odd one
+    constexpr int kG = (kGroups + 1) / 2;
+    const int wq = warp & 3, half = (warp - 4) >> 2, ts = tid - 128;
+    const int g0 = half * kG, ng = half ? kGroups - kG : kG;
+    const int tok = 16 * wq + (lane >> 2), c0 = 2 * (lane & 3);   // tokens tok, tok + 8
     const uint32_t tl = tb + ((uint32_t)(32 * wq) << 16);
-    const bool has_rows = 32 * wq < nr;
     const float c = sh.scale * kLog2e;
     LatentWalk walk(st);
     LatentPiece p;
@@ -391,63 +418,96 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
       return mbar_wait(&bar.pv_done[pl.np == 2 ? t & 1 : 0], (pl.np == 2 ? t >> 1 : t) & 1, kWaitLimit);
     };
     while (!dead && walk.next(sh, seq_lens, cu_seqlens, nr, kTcTile, &p)) {
-      const bool row = r < p.rows;
-      const int lim = min(p.start + (p.row_in_seq + r) / sh.H + 1, p.len);
-      const int low = p.start + p.row_in_seq / sh.H + 1;
-      float m = -INFINITY, l = 0.f;
+      const int low = p.start + p.row_in_seq / sh.H + 1; // the first row's limit, the least
+      if (ts < nr) {                                     // rows behind the block: no weight at all
+        s_m[ts] = ts < p.rows ? kNone : INFINITY;
+        s_more[ts] = (uint8_t)((p.row_in_seq + ts) / sh.H - p.row_in_seq / sh.H);
+      }
+      float l[kG][2];
+#pragma unroll
+      for (int i = 0; i < kG; ++i) l[i][0] = l[i][1] = 0.f;
+      named_bar(1, kSoft);
       for (int t = p.t0; t < p.t1; ++t, ++g) {
-        ok = ok && mbar_wait(&bar.s_full[g & 1], (g >> 1) & 1, kWaitLimit);
+        const uint32_t sb = kSBuf == 2 ? g & 1 : 0;
+        ok = ok && mbar_wait(&bar.s_full[sb], (kSBuf == 2 ? g >> 1 : g) & 1, kWaitLimit);
         tc_fence_after();
-        const int k0 = t * kTcTile + 32 * half;
         const bool mixed = (t + 1) * kTcTile > low;
-        uint32_t s[2][16];
-        bool need = false;
-        float mt = -INFINITY;
-        if (has_rows) {
-          tmem_ld16(tl + kTmemS + (g & 1) * kTcTile + 32 * half, s[0]);
-          tmem_ld16(tl + kTmemS + (g & 1) * kTcTile + 32 * half + 16, s[1]);
-          tmem_wait_ld();
-          if (mixed) {
+        uint32_t s[kG][4];
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (k0 + i >= lim) s[i >> 4][i & 15] = 0xff800000u;      // -inf
-          }
-#pragma unroll
-          for (int i = 0; i < 32; ++i) mt = fmaxf(mt, __uint_as_float(s[i >> 4][i & 15]));
-          mt *= c;                                       // c > 0: the scaled maximum
-          need = row && mt > (m == -INFINITY ? m : m + 8.f);
-          if (r < nr) s_half[half][r] = mt;
-        }
+        for (int i = 0; i < kG; ++i)
+          if (i < ng) tmem_ld_16x256b(tl + kTmemS + sb * nr + 8 * (g0 + i), s[i]);
+        tmem_wait_ld();
         tc_fence_before();
+        if (kSBuf == 1) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.s_empty);
+        }
+        // x = scaled score less the maximum, in place; whether some x passes 2^8
+        float top = -INFINITY;
+        auto less_max = [&](bool first_time) {
+#pragma unroll
+          for (int i = 0; i < kG; ++i)
+            if (i < ng) {
+              const float2 m = s_m2[4 * (g0 + i) + (lane & 3)];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if (first_time && mixed &&
+                    t * kTcTile + tok + 8 * (e >> 1) >=
+                        low + s_more[8 * (g0 + i) + c0 + (e & 1)])
+                  s[i][e] = 0xff800000u;                 // -inf
+                top = fmaxf(top, fmaf(__uint_as_float(s[i][e]), c, -(e & 1 ? m.y : m.x)));
+              }
+            }
+        };
+        less_max(true);
         // rows that some query row does not see: nothing that 0 * would turn into a NaN
         if (mixed) {
           const int first = max(low - t * kTcTile, 0), per = sh.rank / 8;
           for (int i = ts; i < (kTcTile - first) * per; i += kSoft) {
-            const int tok = first + i / per, c8 = i % per, pair = c8 >> 4;
+            const int k = first + i / per, c8 = i % per, pair = c8 >> 4;
             const uint32_t sg = (g * pl.ns + pair / pl.spair) % pl.stages;
             uint4* w = reinterpret_cast<uint4*>(sst + sg * stage_bytes + (pair % pl.spair) * kPair +
-                                                ((c8 >> 3) & 1) * kChunk + tok * 128 +
-                                                (((c8 & 7) ^ (tok & 7)) << 4));
+                                                ((c8 >> 3) & 1) * kChunk + k * 128 + (c8 & 7) * 16);
             const uint4 a = *w;
             const uint4 b = make_uint4(zero_bad(a.x), zero_bad(a.y), zero_bad(a.z), zero_bad(a.w));
             if (a.x != b.x || a.y != b.y || a.z != b.z || a.w != b.w) *w = b;
           }
         }
-        if (named_bar_or(1, kSoft, need || !ok)) {
-          // the first tile, or a maximum that passed: O^T and sums go to the maxima of now
-          float al = 1.f;
-          if (has_rows && row) {
-            const float mn = fmaxf(m, fmaxf(s_half[0][r], s_half[1][r]));
-            if (m != -INFINITY) al = ex2(m - mn);
-            l *= al;
-            m = mn;
+        if (named_bar_or(1, kSoft, top > 8.f || !ok)) {
+          // a maximum that passed (the first tile's always): weights, sums and O^T go to the
+          // maxima of now
+#pragma unroll
+          for (int i = 0; i < kG; ++i)
+            if (i < ng) {
+              float a = fmaxf(__uint_as_float(s[i][0]), __uint_as_float(s[i][2]));
+              float b = fmaxf(__uint_as_float(s[i][1]), __uint_as_float(s[i][3]));
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) {
+                a = fmaxf(a, __shfl_xor_sync(kAll, a, o));
+                b = fmaxf(b, __shfl_xor_sync(kAll, b, o));
+              }
+              if (lane < 4) *reinterpret_cast<float2*>(&s_red[wq][8 * (g0 + i) + c0]) = make_float2(a, b);
+            }
+          named_bar(1, kSoft);
+          if (ts < nr) {
+            const float mo = s_m[ts];
+            const float mn = fmaxf(mo, c * fmaxf(fmaxf(s_red[0][ts], s_red[1][ts]),
+                                                 fmaxf(s_red[2][ts], s_red[3][ts])));
+            s_row[ts] = mo == mn ? 1.f : ex2(mo - mn);
+            s_m[ts] = mn;
           }
-          if (half == 0 && r < nr) s_row[r] = al;
           if (t > p.t0) ok = ok && pv_wait(1);           // the tiles before have been added
           if (named_bar_or(1, kSoft, !ok)) { dead = true; break; }
+#pragma unroll
+          for (int i = 0; i < kG; ++i)
+            if (i < ng) {
+              l[i][0] *= s_row[8 * (g0 + i) + c0];
+              l[i][1] *= s_row[8 * (g0 + i) + c0 + 1];
+            }
           if (t > p.t0) {
             tc_fence_after();
             for (int j = half; j < npair; j += 2)
+#pragma unroll 1
               for (int i = 0; i < nr; i += 16) {
                 uint32_t o[16];
                 tmem_ld16(tl + j * nr + i, o);
@@ -461,26 +521,23 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
             tc_fence_before();
           }
         }
-        if (has_rows) {
-          const float ms = m == -INFINITY ? 0.f : m;
-          if (puse > 0) ok = ok && pv_wait(pl.np);       // the buffer's last values are done
-          uint8_t* const pr = sp + pb * pl.p_bytes + r * 128;
-          float l0 = 0.f, l1 = 0.f;
+        if (puse > 0) ok = ok && pv_wait(pl.np);         // the buffer's last values are done
+        uint8_t* const pr = sp + pb * pl.p_bytes;
 #pragma unroll
-          for (int c8 = 0; c8 < 4; ++c8) {
-            float e[8];
+        for (int i = 0; i < kG; ++i)
+          if (i < ng) {
+            const float2 m = s_m2[4 * (g0 + i) + (lane & 3)];
+            float x[4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              e[i] = row ? ex2(fmaf(__uint_as_float(s[c8 >> 1][8 * (c8 & 1) + i]), c, -ms)) : 0.f;
-            l0 += (e[0] + e[1]) + (e[2] + e[3]);
-            l1 += (e[4] + e[5]) + (e[6] + e[7]);
-            if (r < nr)
-              *reinterpret_cast<uint4*>(pr + (((4 * half + c8) ^ (r & 7)) << 4)) =
-                  make_uint4(pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3]), pack_bf16(e[4], e[5]),
-                             pack_bf16(e[6], e[7]));
+            for (int e = 0; e < 4; ++e)
+              x[e] = ex2(fmaf(__uint_as_float(s[i][e]), c, -(e & 1 ? m.y : m.x)));
+            l[i][0] += x[0] + x[2];
+            l[i][1] += x[1] + x[3];
+            const uint32_t n = 8 * (g0 + i) + c0;
+            *reinterpret_cast<uint32_t*>(pr + off_mnmajor_sw32(n, tok, kTcTile)) = pack_bf16(x[0], x[1]);
+            *reinterpret_cast<uint32_t*>(pr + off_mnmajor_sw32(n, tok + 8, kTcTile)) =
+                pack_bf16(x[2], x[3]);
           }
-          l += l0 + l1;
-        }
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.p_full[pb]);
@@ -493,15 +550,25 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
       // ---- results: whole blocks to the output, shared ones to a partial slot
       const bool first = p.t0 == 0, last = p.t1 == p.tiles;
       const int slot = first && last ? -1 : 2 * (int)blockIdx.x + (first ? 1 : 0);
-      if (r < nr) s_half[half][r] = l;
+#pragma unroll
+      for (int i = 0; i < kG; ++i)
+        if (i < ng) {
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) {
+            l[i][0] += __shfl_xor_sync(kAll, l[i][0], o);
+            l[i][1] += __shfl_xor_sync(kAll, l[i][1], o);
+          }
+          if (lane < 4)
+            *reinterpret_cast<float2*>(&s_red[wq][8 * (g0 + i) + c0]) = make_float2(l[i][0], l[i][1]);
+        }
       ok = ok && pv_wait(1);
       if (named_bar_or(1, kSoft, !ok)) break;
-      if (half == 0 && r < nr) {
-        l += s_half[1][r];
-        s_row[r] = l == 0.f ? 0.f : 1.0f / l;
-        const float z = l == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m) * kLn2 + logf(l);
-        if (slot >= 0) pt.lse[slot * nr + r] = z;
-        else if (lse && row) lse[p.row0 + r] = z;
+      if (ts < nr) {
+        const float z = (s_red[0][ts] + s_red[1][ts]) + (s_red[2][ts] + s_red[3][ts]);
+        s_row[ts] = z == 0.f ? 0.f : 1.0f / z;
+        const float y = z == 0.f ? -INFINITY : s_m[ts] * kLn2 + logf(z);
+        if (slot >= 0) pt.lse[slot * nr + ts] = y;
+        else if (lse && ts < p.rows) lse[p.row0 + ts] = y;
       }
       if (slot >= 0 && first && ts == 0)
         pt.head[blockIdx.x] =
@@ -509,7 +576,8 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
       named_bar(1, kSoft);
       tc_fence_after();
       for (int j = half; j < npair; j += 2) {
-        const int d = 128 * j + r;
+        const int d = 128 * j + 32 * wq + lane;
+#pragma unroll 1
         for (int i = 0; i < p.rows; i += 16) {
           uint32_t o[16];
           tmem_ld16(tl + j * nr + i, o);
@@ -530,7 +598,7 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
         }
       }
       tc_fence_before();
-      named_bar(1, kSoft);                               // s_row and s_half are free again
+      named_bar(1, kSoft);                               // the block's rows are done with
       if (lane == 0) mbar_arrive(&bar.o_empty);
     }
   }
@@ -541,6 +609,19 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tb, kTmemCols);
+  }
+}
+
+using TcKernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, const int32_t*, const int32_t*,
+                          const int32_t*, bf16*, float*, LatentAttnShape, TcPlan, LatentPartials);
+TcKernel tc_kernel(int nr) {
+  switch (nr) {
+    case 16: return kda_latent_tc_kernel<16>;
+    case 32: return kda_latent_tc_kernel<32>;
+    case 48: return kda_latent_tc_kernel<48>;
+    case 64: return kda_latent_tc_kernel<64>;
+    case 80: return kda_latent_tc_kernel<80>;
+    default: return kda_latent_tc_kernel<96>;
   }
 }
 
@@ -567,9 +648,11 @@ cudaError_t launch_latent_tc(const void* q, const void* cache, const int32_t* pa
                              float* lse, const LatentAttnShape& sh, int sms, void* buf,
                              cudaStream_t stream) {
   if (!once_per_device(kOnceLatentTc, []() {
-        return cudaFuncSetAttribute(kda_latent_tc_kernel,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (int)kTcSmem + 1024) == cudaSuccess;
+        for (int nr = 16; nr <= kTcMaxRows; nr += 16)
+          if (cudaFuncSetAttribute(tc_kernel(nr), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   (int)kTcSmem) != cudaSuccess)
+            return false;
+        return true;
       }))
     return cudaErrorInvalidDevice;
   const int nr = tc_rows(sh.N, sh.L, sh.T, sh.H), G = latent_tc_ctas(sms);
@@ -587,7 +670,7 @@ cudaError_t launch_latent_tc(const void* q, const void* cache, const int32_t* pa
       !cache_map(&c_map, 2) || !cache_map(&r_map, 1))
     return cudaErrorInvalidValue;
   KDA_TIMED(KDA_KERNEL_LATENT_ATTN, stream,
-            kda_latent_tc_kernel<<<G, kTcThreads, kTcSmem + 1024, stream>>>(
+            tc_kernel(nr)<<<G, kTcThreads, kTcSmem, stream>>>(
                 q_map, c_map, r_map, page_table, seq_lens, cu_seqlens, static_cast<bf16*>(out), lse, sh,
                 pl, pt));
   const cudaError_t e = cudaGetLastError();
