@@ -249,13 +249,20 @@ def _decay_group(g: torch.Tensor, dk: int) -> int:
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
-def _stream(stream) -> ctypes.c_void_p:
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+# The current stream's handle without a Stream object around it: 0.07 us a call, not 3.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(stream) -> int:
+    """Handle of `stream`, by default of the current device's current stream."""
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _check(name: str, t: torch.Tensor, dtype=None, shape=None):
@@ -558,21 +565,21 @@ def kda_decode_chunk(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch
 
 # ------------------------------------------------ latent attention, drafted tokens
 
-def _run_on(device: torch.device, stream, call, fn: str) -> None:
-    """call(stream handle) with `device` current (the library works on the current one)."""
+def _run_on(device: torch.device, stream, fn, args, name: str) -> None:
+    """fn(*args, stream handle) with `device` current (the library works on the current one)."""
     if device.index != torch.cuda.current_device():
         with torch.cuda.device(device):
-            rc = call(_stream(stream))
+            rc = fn(*args, _stream(stream))
     else:
-        rc = call(_stream(stream))
+        rc = fn(*args, _stream(stream))
     if rc != KDA_OK:
-        raise KdaError(fn, rc)
+        raise KdaError(name, rc)
 
 
-def _same_device(device: torch.device, **tensors) -> None:
-    for name, t in tensors.items():
+def _same_device(device: torch.device, *tensors) -> None:
+    for t in tensors:
         if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
+            raise ValueError(f"tensors on {t.device} and on {device} in one call")
 
 
 def _latent_args(B: int, T: int, D: int, dtype, kv_cache: torch.Tensor, page_table: torch.Tensor,
@@ -649,16 +656,15 @@ def kda_latent_append(kv: torch.Tensor, kv_cache: torch.Tensor, page_table: torc
                 raise ValueError(f"{name} must be a CUDA tensor with contiguous rows")
             qs[2 * i] = _token_stride(name, t) or H * rope
             qs[2 * i + 1] = t.stride(2) if H > 1 else rope
-    _same_device(kv.device, kv_cache=kv_cache, page_table=page_table, seq_lens=seq_lens,
-                 cu_seqlens=cu_seqlens, norm_weight=norm_weight, inv_freq=inv_freq, q_pe=q_pe,
-                 q_pe_out=q_pe_out)
-    L_ = lib()
-    _run_on(kv.device, stream, lambda st: L_.kda_latent_append(
-        _ptr(kv), _ptr(norm_weight), _ptr(inv_freq), _ptr(q_pe), _ptr(q_pe_out), _ptr(kv_cache),
-        _ptr(page_table), _ptr(seq_lens), _ptr(cu_seqlens), nseq, T, H, rank, rope,
-        kv_cache.shape[0], kv_cache.shape[1], page_table.shape[1], kv_cache.stride(0),
-        kv_cache.stride(1), _token_stride("kv", kv) or D, *qs, eps, int(interleaved), dt, st),
-        "kda_latent_append")
+    _same_device(kv.device, kv_cache, page_table, seq_lens, cu_seqlens, norm_weight, inv_freq, q_pe,
+                 q_pe_out)
+    pages, page_size, _ = kv_cache.shape
+    page_stride, row_stride, _ = kv_cache.stride()
+    _run_on(kv.device, stream, lib().kda_latent_append,
+            (_ptr(kv), _ptr(norm_weight), _ptr(inv_freq), _ptr(q_pe), _ptr(q_pe_out),
+             _ptr(kv_cache), _ptr(page_table), _ptr(seq_lens), _ptr(cu_seqlens), nseq, T, H, rank,
+             rope, pages, page_size, page_table.shape[1], page_stride, row_stride,
+             _token_stride("kv", kv) or D, *qs, eps, int(interleaved), dt), "kda_latent_append")
     return q_pe_out
 
 
@@ -694,24 +700,24 @@ def kda_latent_attn(q: torch.Tensor, kv_cache: torch.Tensor, page_table: torch.T
     dt, nseq, rope = _latent_args(B, T, D, q.dtype, kv_cache, page_table, seq_lens, cu_seqlens,
                                   rank)
     if out is None:
-        out = torch.empty((B, T, H, rank), dtype=q.dtype, device=q.device)
+        out = q.new_empty((B, T, H, rank))
     else:
         _check("out", out, q.dtype, (B, T, H, rank))
     if lse is None:
         lse = torch.empty((B, T, H), dtype=torch.float32, device=q.device)
     else:
         _check("lse", lse, torch.float32, (B, T, H))
-    _same_device(q.device, kv_cache=kv_cache, page_table=page_table, seq_lens=seq_lens,
-                 cu_seqlens=cu_seqlens, out=out, lse=lse, workspace=workspace)
-    args = [_ptr(q), _ptr(kv_cache), _ptr(page_table), _ptr(seq_lens), _ptr(cu_seqlens), _ptr(out),
-            _ptr(lse), nseq, T, H, rank, rope, kv_cache.shape[0], kv_cache.shape[1],
-            page_table.shape[1], kv_cache.stride(0), kv_cache.stride(1), scale, dt]
-    L_ = lib()
+    _same_device(q.device, kv_cache, page_table, seq_lens, cu_seqlens, out, lse, workspace)
+    pages, page_size, _ = kv_cache.shape
+    page_stride, row_stride, _ = kv_cache.stride()
+    args = (_ptr(q), _ptr(kv_cache), _ptr(page_table), _ptr(seq_lens), _ptr(cu_seqlens), _ptr(out),
+            _ptr(lse), nseq, T, H, rank, rope, pages, page_size, page_table.shape[1], page_stride,
+            row_stride, scale, dt)
     if workspace is not None:
-        args += _workspace_args(workspace)
-        _run_on(q.device, stream, lambda st: L_.kda_latent_attn_ws(*args, st), "kda_latent_attn_ws")
+        _run_on(q.device, stream, lib().kda_latent_attn_ws, args + _workspace_args(workspace),
+                "kda_latent_attn_ws")
     else:
-        _run_on(q.device, stream, lambda st: L_.kda_latent_attn(*args, st), "kda_latent_attn")
+        _run_on(q.device, stream, lib().kda_latent_attn, args, "kda_latent_attn")
     return out, lse
 
 
@@ -737,17 +743,15 @@ def kda_verify_tokens(target: torch.Tensor, draft: Optional[torch.Tensor],
     if draft_lens is not None:
         _check("draft_lens", draft_lens, torch.int32, (N,))
     if tokens is None:
-        tokens = torch.empty((N, L1), dtype=torch.int32, device=target.device)
+        tokens = draft_tokens.new_empty((N, L1))
     else:
         _check("tokens", tokens, torch.int32, (N, L1))
     if accepted is None:
-        accepted = torch.empty((N,), dtype=torch.int32, device=target.device)
+        accepted = draft_tokens.new_empty((N,))
     else:
         _check("accepted", accepted, torch.int32, (N,))
-    _same_device(target.device, draft=draft, draft_tokens=draft_tokens, uniforms=uniforms,
-                 draft_lens=draft_lens, tokens=tokens, accepted=accepted)
-    L_ = lib()
-    _run_on(target.device, stream, lambda st: L_.kda_verify_tokens(
-        _ptr(target), _ptr(draft), _ptr(draft_tokens), _ptr(uniforms), _ptr(draft_lens),
-        _ptr(tokens), _ptr(accepted), N, L, V, st), "kda_verify_tokens")
+    _same_device(target.device, draft, draft_tokens, uniforms, draft_lens, tokens, accepted)
+    _run_on(target.device, stream, lib().kda_verify_tokens,
+            (_ptr(target), _ptr(draft), _ptr(draft_tokens), _ptr(uniforms), _ptr(draft_lens),
+             _ptr(tokens), _ptr(accepted), N, L, V), "kda_verify_tokens")
     return tokens, accepted

@@ -9,12 +9,13 @@
 //
 // Bound by memory: of all the rows given, one target row and (after a rejection) one draft
 // row a sequence are read.  A cluster of C CTAs shares a sequence, each warp summing one
-// contiguous stretch of the vocabulary; the stretches' sums meet in the first CTA's shared
-// memory, whose first warp finds the stretch that the threshold falls into and reads that
-// one again, lane by lane.  No atomics: the same inputs give the same tokens.  C is the
-// largest of 1, 2, 4, 8 whose CTAs are all resident at once (four an SM) and whose
-// stretches stay above 256 elements: one sequence of 32,000 then takes eight SMs, 256
-// sequences two CTAs each.
+// four neighbouring stretches of the vocabulary; the stretches' sums meet in the first CTA's
+// shared memory, whose first warp finds the stretch that the threshold falls into and reads
+// that one again, 256 elements at a time and the last of them lane by lane.  No atomics:
+// the same inputs give the same tokens.  C is the largest of 1, 2, 4, 8 whose CTAs are all
+// resident at once (four an SM, for eight loads of each row in flight a lane) and whose
+// stretches stay above 64 elements.  Apart from the rows' bytes a call costs four dependent
+// trips to memory (drafts, their probabilities, the row, the stretch again).
 #include <cooperative_groups.h>
 
 #include "kda_common.cuh"
@@ -24,23 +25,44 @@ namespace kda {
 namespace {
 namespace cg = cooperative_groups;
 
-constexpr int kVT = 512;                 // threads of a CTA
+constexpr int kVT = 256;                 // threads of a CTA
 constexpr int kVW = kVT / 32;
+constexpr int kVPerSm = 4;               // resident CTAs of an SM
+constexpr int kSub = 4;                  // stretches of a warp
 constexpr int kMaxCluster = 8;
-constexpr int kUnroll = 8;
+constexpr int kUnroll = 8, kBlock = 32 * kUnroll;
 
-// Weight of element v: what the target has over the draft, never below zero; a NaN is none.
+// Weight of an element: what the target has over the draft, never below zero; a NaN is none.
 __device__ __forceinline__ double weight(float p, float q) {
-  const double d = (double)p - (double)q;
-  return d > 0.0 ? d : 0.0;
+  const bool over = p > q;
+  return (double)(over ? p : 0.f) - (double)(over ? q : 0.f);
 }
 
-__global__ void __launch_bounds__(kVT)
+// This lane's share of the weights of [v0, v1).
+template <bool kDraft>
+__device__ __forceinline__ double lane_sum(const float* p, const float* q, int v0, int v1, int lane) {
+  double sum = 0.0;
+  for (int v = v0 + lane; v < v1; v += kBlock) {
+    float pv[kUnroll], qv[kUnroll];
+    const bool whole = v - lane + kBlock <= v1;
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      const bool in = whole || v + 32 * i < v1;
+      pv[i] = in ? __ldg(p + v + 32 * i) : 0.f;
+      qv[i] = kDraft && in ? __ldg(q + v + 32 * i) : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) sum += weight(pv[i], qv[i]);
+  }
+  return sum;
+}
+
+__global__ void __launch_bounds__(kVT, kVPerSm)
 kda_verify_kernel(const float* __restrict__ target, const float* __restrict__ draft,
                   const int32_t* __restrict__ draft_tokens, const float* __restrict__ uniforms,
                   const int32_t* __restrict__ draft_lens, int32_t* __restrict__ tokens,
                   int32_t* __restrict__ accepted, int L, int V) {
-  __shared__ double s_sum[kMaxCluster * kVW];       // the first CTA's: every stretch's sum
+  __shared__ double s_sum[kMaxCluster * kVW * kSub];   // the first CTA's: every stretch's sum
   __shared__ int s_acc;
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -78,34 +100,40 @@ kda_verify_kernel(const float* __restrict__ target, const float* __restrict__ dr
   const int xr = rejected ? __ldg(xs + a) : -1;      // without draft rows: its weight is zero
   const int cut = rejected && !draft ? xr : -1;
 
-  // ---- this warp's stretch [v0, v1)
-  const int S = C * kVW;
+  // ---- this warp's stretches
+  const int S = C * kVW * kSub;
   const int len = (V + S - 1) / S;
-  const int v0 = (int)min((long long)(rank * kVW + warp) * len, (long long)V);
-  const int v1 = (int)min((long long)v0 + len, (long long)V);
-  double sum = 0.0;
-  for (int v = v0 + lane; v < v1; v += 32 * kUnroll) {
-    float pv[kUnroll], qv[kUnroll];
+  const int st0 = (rank * kVW + warp) * kSub;
+  double sum[kSub];
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-      const bool in = v + 32 * i < v1;
-      pv[i] = in ? __ldg(p + v + 32 * i) : 0.f;
-      qv[i] = in && q ? __ldg(q + v + 32 * i) : 0.f;
+  for (int i = 0; i < kSub; ++i) {
+    const int v0 = (int)min((long long)(st0 + i) * len, (long long)V);
+    const int v1 = (int)min((long long)v0 + len, (long long)V);
+    if (q) {
+      sum[i] = lane_sum<true>(p, q, v0, v1, lane);
+    } else if (cut >= v0 && cut < v1) {
+      sum[i] = lane_sum<false>(p, q, v0, cut, lane) + lane_sum<false>(p, q, cut + 1, v1, lane);
+    } else {
+      sum[i] = lane_sum<false>(p, q, v0, v1, lane);
     }
-#pragma unroll
-    for (int i = 0; i < kUnroll; ++i) sum += v + 32 * i == cut ? 0.0 : weight(pv[i], qv[i]);
   }
 #pragma unroll
-  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  for (int i = 0; i < kSub; ++i)
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
   cluster.barrier_wait();
-  if (lane == 0) *cluster.map_shared_rank(&s_sum[rank * kVW + warp], 0) = sum;
+  if (lane == 0) {
+    double* d = cluster.map_shared_rank(&s_sum[st0], 0);
+#pragma unroll
+    for (int i = 0; i < kSub; ++i) d[i] = sum[i];
+  }
   cluster.barrier_arrive();
   if (rank != 0) return;                             // nothing of this CTA is read by another
   cluster.barrier_wait();
   if (warp != 0) return;
 
-  // ---- the first stretch whose running sum passes u * total (S <= 128: four a lane)
-  constexpr int P = kMaxCluster * kVW / 32;
+  // ---- the first stretch whose running sum passes u * total (S <= 256: eight a lane)
+  constexpr int P = kMaxCluster * kVW * kSub / 32;
   double part[P], mine = 0.0;
 #pragma unroll
   for (int i = 0; i < P; ++i) {
@@ -144,19 +172,42 @@ kda_verify_kernel(const float* __restrict__ target, const float* __restrict__ dr
     before = __shfl_sync(0xffffffffu, before, src);
     const int b0 = (int)min((long long)st * len, (long long)V);
     const int b1 = (int)min((long long)b0 + len, (long long)V);
-    for (int v = b0; v < b1; v += 32 * kUnroll) {
-      float pv[kUnroll], qv[kUnroll];
+    // its first block of 256 whose running sum passes (or the last with any weight)
+    constexpr int kB = kUnroll;
+    float pv[kB], qv[kB];
+    auto load = [&](int v) {
 #pragma unroll
-      for (int i = 0; i < kUnroll; ++i) {
+      for (int i = 0; i < kB; ++i) {
         const int e = v + 32 * i + lane;
-        pv[i] = e < b1 ? __ldg(p + e) : 0.f;
-        qv[i] = e < b1 && q ? __ldg(q + e) : 0.f;
+        const bool in = e < b1 && e != cut;
+        pv[i] = in ? __ldg(p + e) : 0.f;
+        qv[i] = in && q ? __ldg(q + e) : 0.f;
       }
+    };
+    int at = -1;
+    double at_before = 0.0;
+    bool passed = false;
+    load(b0);
+    for (int v = b0; v < b1 && !passed; v += kBlock) {
+      double bs = 0.0;
+#pragma unroll
+      for (int i = 0; i < kB; ++i) bs += weight(pv[i], qv[i]);
+      if (v + kBlock < b1) load(v + kBlock);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) bs += __shfl_xor_sync(0xffffffffu, bs, o);
+      if (bs > 0.0) {
+        at = v;
+        at_before = before;
+        passed = hits && before + bs > thr;
+      }
+      before += bs;
+    }
+    if (at >= 0) {
+      load(at);
       bool done = false;
 #pragma unroll
-      for (int i = 0; i < kUnroll; ++i) {
-        const int e = v + 32 * i + lane;
-        const double wv = e == cut ? 0.0 : weight(pv[i], qv[i]);
+      for (int i = 0; i < kB; ++i) {
+        const double wv = weight(pv[i], qv[i]);
         double r = wv;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -164,12 +215,11 @@ kda_verify_kernel(const float* __restrict__ target, const float* __restrict__ dr
           if (lane >= o) r += up;
         }
         const unsigned some = __ballot_sync(0xffffffffu, wv > 0.0);
-        const unsigned over = __ballot_sync(0xffffffffu, wv > 0.0 && hits && before + r > thr);
-        if (!done && some) tok = v + 32 * i + (over ? __ffs(over) - 1 : 31 - __clz(some));
+        const unsigned over = __ballot_sync(0xffffffffu, wv > 0.0 && passed && at_before + r > thr);
+        if (!done && some) tok = at + 32 * i + (over ? __ffs(over) - 1 : 31 - __clz(some));
         done = done || over;
-        before += __shfl_sync(0xffffffffu, r, 31);
+        at_before += __shfl_sync(0xffffffffu, r, 31);
       }
-      if (done) break;
     }
   } else if (rejected && xr >= 0 && xr < V) {
     tok = xr;                                        // p = q up to rounding: the draft is a draw of p
@@ -188,7 +238,8 @@ cudaError_t launch_verify_tokens(const float* target, const float* draft,
   int sms = 0;
   if (!device_ctx(&sms, nullptr)) return cudaErrorInvalidDevice;
   int C = 1;
-  while (C < kMaxCluster && 2LL * C * N <= 4LL * sms && V >= 2 * C * kVW * 256) C *= 2;
+  while (C < kMaxCluster && 2LL * C * N <= (long long)kVPerSm * sms && V >= 2 * C * kVW * kSub * 64)
+    C *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(N * C));
   cfg.blockDim = dim3(kVT);
