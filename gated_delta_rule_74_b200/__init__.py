@@ -565,10 +565,10 @@ def kda_decode_chunk(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch
 
 # ------------------------------------------------ latent attention, drafted tokens
 
-def _run_on(device: torch.device, stream, fn, args, name: str) -> None:
-    """fn(*args, stream handle) with `device` current (the library works on the current one)."""
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
+def _run_on(dev: int, stream, fn, args, name: str) -> None:
+    """fn(*args, stream handle) with device `dev` current (the library works on that one)."""
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
             rc = fn(*args, _stream(stream))
     else:
         rc = fn(*args, _stream(stream))
@@ -576,44 +576,67 @@ def _run_on(device: torch.device, stream, fn, args, name: str) -> None:
         raise KdaError(name, rc)
 
 
-def _same_device(device: torch.device, *tensors) -> None:
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"tensors on {t.device} and on {device} in one call")
+def _device_of(name: str, t: torch.Tensor) -> int:
+    dev = t.get_device()
+    if dev < 0 or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return dev
 
 
-def _latent_args(B: int, T: int, D: int, dtype, kv_cache: torch.Tensor, page_table: torch.Tensor,
-                 seq_lens: torch.Tensor, cu_seqlens: Optional[torch.Tensor], rank: int):
-    """Checks shared by kda_latent_append and kda_latent_attn; (dtype id, sequences, rope)."""
+def _take(name: str, t: Optional[torch.Tensor], dev: int, dtype, shape) -> Optional[int]:
+    """Pointer of an optional contiguous tensor on device `dev`; one test for all of it, as a
+    decode step's calls are as short as their checks."""
+    if t is None:
+        return None
+    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        _check(name, t, dtype, shape)
+        raise ValueError(f"{name} is on {t.device}, the call's other tensors on cuda:{dev}")
+    return t.data_ptr()
+
+
+def _latent_args(B: int, T: int, D: int, dtype, dev: int, kv_cache: torch.Tensor,
+                 page_table: torch.Tensor, seq_lens: torch.Tensor,
+                 cu_seqlens: Optional[torch.Tensor], rank: int):
+    """Checks shared by kda_latent_append and kda_latent_attn: (dtype id, the pointers of
+    cache, table, lengths and offsets, sequences, cache and table sizes and strides)."""
     dt = _DTYPES.get(dtype)
     if dt is None:
         raise ValueError(f"unsupported dtype {dtype}")
-    if kv_cache.dim() != 3 or kv_cache.shape[2] != D or kv_cache.dtype != dtype:
+    if not 0 < rank <= D:
+        raise ValueError(f"rank {rank} does not fit rows of {D}")
+    if kv_cache.dim() != 3 or kv_cache.shape[2] != D or kv_cache.dtype is not dtype:
         raise ValueError(f"kv_cache must be [pages, page_size, {D}] of {dtype}, got "
                          f"{tuple(kv_cache.shape)} of {kv_cache.dtype}")
-    if not kv_cache.is_cuda or kv_cache.stride(2) != 1:
-        raise ValueError("kv_cache must be a CUDA tensor with contiguous rows")
-    _check("seq_lens", seq_lens, torch.int32)
+    page_stride, row_stride, one = kv_cache.stride()
+    if kv_cache.get_device() != dev or one != 1:
+        raise ValueError(f"kv_cache must be a tensor on cuda:{dev} with contiguous rows")
     nseq = seq_lens.numel()
+    lens = _take("seq_lens", seq_lens, dev, torch.int32, (nseq,))
+    cu = None
     if cu_seqlens is not None:
-        _check("cu_seqlens", cu_seqlens, torch.int32, (nseq + 1,))
+        cu = _take("cu_seqlens", cu_seqlens, dev, torch.int32, (nseq + 1,))
         if B != 1:
             raise ValueError("packed inputs (cu_seqlens) must have B == 1")
     elif nseq != B:
         raise ValueError(f"seq_lens has {nseq} entries for {B} sequences")
-    _check("page_table", page_table, torch.int32)
-    if page_table.dim() != 2 or page_table.shape[0] != nseq:
+    if page_table.dim() != 2:
         raise ValueError(f"page_table must be [{nseq}, max_pages], got {tuple(page_table.shape)}")
-    if not 0 < rank <= D:
-        raise ValueError(f"rank {rank} does not fit rows of {D}")
-    return dt, nseq, D - rank
+    most = page_table.shape[1]
+    table = _take("page_table", page_table, dev, torch.int32, (nseq, most))
+    pages, page_size, _ = kv_cache.shape
+    return (dt, kv_cache.data_ptr(), table, lens, cu, nseq,
+            (pages, page_size, most, page_stride, row_stride))
 
 
-def _token_stride(name: str, t: torch.Tensor) -> int:
-    """Elements from one token of t [B, T, ..] to the next, which has to hold across B."""
-    if t.shape[0] > 1 and t.shape[1] > 1 and t.stride(0) != t.shape[1] * t.stride(1):
-        raise ValueError(f"{name}'s sequences must follow each other at its token stride")
-    return t.stride(1) if t.shape[1] > 1 else t.stride(0) if t.shape[0] > 1 else 0
+def _token_stride(name: str, t: torch.Tensor, dense: int) -> int:
+    """Elements from one token of t [B, T, ..] to the next, which has to hold across B
+    (`dense` where there is but one token)."""
+    B, T = t.shape[:2]
+    if T > 1:
+        if B > 1 and t.stride(0) != T * t.stride(1):
+            raise ValueError(f"{name}'s sequences must follow each other at its token stride")
+        return t.stride(1)
+    return t.stride(0) if B > 1 else dense
 
 
 def kda_latent_append(kv: torch.Tensor, kv_cache: torch.Tensor, page_table: torch.Tensor,
@@ -633,38 +656,33 @@ def kda_latent_append(kv: torch.Tensor, kv_cache: torch.Tensor, page_table: torc
     if kv.dim() != 3:
         raise ValueError("kv must be [B, T, rank + rope]")
     B, T, D = kv.shape
-    dt, nseq, rope = _latent_args(B, T, D, kv.dtype, kv_cache, page_table, seq_lens, cu_seqlens,
-                                  rank)
-    if not kv.is_cuda or kv.stride(2) != 1:
-        raise ValueError("kv must be a CUDA tensor with contiguous rows")
-    if norm_weight is not None:
-        _check("norm_weight", norm_weight, torch.float32, (rank,))
-    if inv_freq is not None:
-        _check("inv_freq", inv_freq, torch.float32, (rope // 2,))
-    H, qs = 1, [0, 0, 0, 0]
-    if q_pe is None and q_pe_out is not None:
-        raise ValueError("q_pe_out needs q_pe")
+    dev = _device_of("kv", kv)
+    dt, cache, table, lens, cu, nseq, (pages, page_size, most, page_stride, row_stride) = \
+        _latent_args(B, T, D, kv.dtype, dev, kv_cache, page_table, seq_lens, cu_seqlens, rank)
+    rope = D - rank
+    if kv.stride(2) != 1:
+        raise ValueError("kv must have contiguous rows")
+    H, qs = 1, (0, 0, 0, 0)
     if q_pe is not None:
         if q_pe_out is None:
             q_pe_out = torch.empty(q_pe.shape, dtype=q_pe.dtype, device=q_pe.device)
         H = q_pe.shape[2] if q_pe.dim() == 4 else 0
-        for i, (name, t) in enumerate((("q_pe", q_pe), ("q_pe_out", q_pe_out))):
-            if t.dim() != 4 or tuple(t.shape) != (B, T, H, rope) or t.dtype != kv.dtype:
+        for name, t in (("q_pe", q_pe), ("q_pe_out", q_pe_out)):
+            if t.shape != (B, T, H, rope) or t.dtype is not kv.dtype:
                 raise ValueError(f"{name} must be [{B}, {T}, H, {rope}] of {kv.dtype}, got "
                                  f"{tuple(t.shape)} of {t.dtype}")
-            if not t.is_cuda or t.stride(3) != 1:
-                raise ValueError(f"{name} must be a CUDA tensor with contiguous rows")
-            qs[2 * i] = _token_stride(name, t) or H * rope
-            qs[2 * i + 1] = t.stride(2) if H > 1 else rope
-    _same_device(kv.device, kv_cache, page_table, seq_lens, cu_seqlens, norm_weight, inv_freq, q_pe,
-                 q_pe_out)
-    pages, page_size, _ = kv_cache.shape
-    page_stride, row_stride, _ = kv_cache.stride()
-    _run_on(kv.device, stream, lib().kda_latent_append,
-            (_ptr(kv), _ptr(norm_weight), _ptr(inv_freq), _ptr(q_pe), _ptr(q_pe_out),
-             _ptr(kv_cache), _ptr(page_table), _ptr(seq_lens), _ptr(cu_seqlens), nseq, T, H, rank,
-             rope, pages, page_size, page_table.shape[1], page_stride, row_stride,
-             _token_stride("kv", kv) or D, *qs, eps, int(interleaved), dt), "kda_latent_append")
+            if t.get_device() != dev or t.stride(3) != 1:
+                raise ValueError(f"{name} must be a tensor on cuda:{dev} with contiguous rows")
+        qs = (_token_stride("q_pe", q_pe, H * rope), q_pe.stride(2) if H > 1 else rope,
+              _token_stride("q_pe_out", q_pe_out, H * rope), q_pe_out.stride(2) if H > 1 else rope)
+    elif q_pe_out is not None:
+        raise ValueError("q_pe_out needs q_pe")
+    _run_on(dev, stream, lib().kda_latent_append,
+            (kv.data_ptr(), _take("norm_weight", norm_weight, dev, torch.float32, (rank,)),
+             _take("inv_freq", inv_freq, dev, torch.float32, (rope // 2,)), _ptr(q_pe),
+             _ptr(q_pe_out), cache, table, lens, cu, nseq, T, H, rank, rope, pages, page_size, most,
+             page_stride, row_stride, _token_stride("kv", kv, D), *qs, eps, interleaved, dt),
+            "kda_latent_append")
     return q_pe_out
 
 
@@ -696,28 +714,25 @@ def kda_latent_attn(q: torch.Tensor, kv_cache: torch.Tensor, page_table: torch.T
     if q.dim() != 4:
         raise ValueError("q must be [B, T, H, rank + rope]")
     B, T, H, D = q.shape
-    _check("q", q)
-    dt, nseq, rope = _latent_args(B, T, D, q.dtype, kv_cache, page_table, seq_lens, cu_seqlens,
-                                  rank)
+    dev = _device_of("q", q)
+    if not q.is_contiguous():
+        raise ValueError("q must be contiguous")
+    dt, cache, table, lens, cu, nseq, (pages, page_size, most, page_stride, row_stride) = \
+        _latent_args(B, T, D, q.dtype, dev, kv_cache, page_table, seq_lens, cu_seqlens, rank)
     if out is None:
         out = q.new_empty((B, T, H, rank))
-    else:
-        _check("out", out, q.dtype, (B, T, H, rank))
     if lse is None:
         lse = torch.empty((B, T, H), dtype=torch.float32, device=q.device)
-    else:
-        _check("lse", lse, torch.float32, (B, T, H))
-    _same_device(q.device, kv_cache, page_table, seq_lens, cu_seqlens, out, lse, workspace)
-    pages, page_size, _ = kv_cache.shape
-    page_stride, row_stride, _ = kv_cache.stride()
-    args = (_ptr(q), _ptr(kv_cache), _ptr(page_table), _ptr(seq_lens), _ptr(cu_seqlens), _ptr(out),
-            _ptr(lse), nseq, T, H, rank, rope, pages, page_size, page_table.shape[1], page_stride,
-            row_stride, scale, dt)
+    args = (q.data_ptr(), cache, table, lens, cu, _take("out", out, dev, q.dtype, (B, T, H, rank)),
+            _take("lse", lse, dev, torch.float32, (B, T, H)), nseq, T, H, rank, D - rank, pages,
+            page_size, most, page_stride, row_stride, scale, dt)
     if workspace is not None:
-        _run_on(q.device, stream, lib().kda_latent_attn_ws, args + _workspace_args(workspace),
+        if workspace.get_device() != dev:
+            raise ValueError(f"workspace must be on cuda:{dev}")
+        _run_on(dev, stream, lib().kda_latent_attn_ws, args + _workspace_args(workspace),
                 "kda_latent_attn_ws")
     else:
-        _run_on(q.device, stream, lib().kda_latent_attn, args, "kda_latent_attn")
+        _run_on(dev, stream, lib().kda_latent_attn, args, "kda_latent_attn")
     return out, lse
 
 
@@ -735,23 +750,17 @@ def kda_verify_tokens(target: torch.Tensor, draft: Optional[torch.Tensor],
         raise ValueError("target must be [N, L + 1, V]")
     N, L1, V = target.shape
     L = L1 - 1
-    _check("target", target, torch.float32)
-    if draft is not None:
-        _check("draft", draft, torch.float32, (N, L, V))
-    _check("draft_tokens", draft_tokens, torch.int32, (N, L))
-    _check("uniforms", uniforms, torch.float32, (N, L1))
-    if draft_lens is not None:
-        _check("draft_lens", draft_lens, torch.int32, (N,))
+    dev = _device_of("target", target)
     if tokens is None:
         tokens = draft_tokens.new_empty((N, L1))
-    else:
-        _check("tokens", tokens, torch.int32, (N, L1))
     if accepted is None:
         accepted = draft_tokens.new_empty((N,))
-    else:
-        _check("accepted", accepted, torch.int32, (N,))
-    _same_device(target.device, draft, draft_tokens, uniforms, draft_lens, tokens, accepted)
-    _run_on(target.device, stream, lib().kda_verify_tokens,
-            (_ptr(target), _ptr(draft), _ptr(draft_tokens), _ptr(uniforms), _ptr(draft_lens),
-             _ptr(tokens), _ptr(accepted), N, L, V), "kda_verify_tokens")
+    _run_on(dev, stream, lib().kda_verify_tokens,
+            (_take("target", target, dev, torch.float32, (N, L1, V)),
+             _take("draft", draft, dev, torch.float32, (N, L, V)),
+             _take("draft_tokens", draft_tokens, dev, torch.int32, (N, L)),
+             _take("uniforms", uniforms, dev, torch.float32, (N, L1)),
+             _take("draft_lens", draft_lens, dev, torch.int32, (N,)),
+             _take("tokens", tokens, dev, torch.int32, (N, L1)),
+             _take("accepted", accepted, dev, torch.int32, (N,)), N, L, V), "kda_verify_tokens")
     return tokens, accepted

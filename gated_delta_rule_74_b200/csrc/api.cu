@@ -321,7 +321,7 @@ int latent_shape_ok(int N, int L, int H, int rank, int rope, int num_pages, int 
   if (N < 1 || L < 0 || H < 1) return KDA_ERR_INVALID_ARG;
   if (dtype != KDA_BF16 && dtype != KDA_F32) return KDA_ERR_INVALID_ARG;
   if (num_pages < 1 || page_size < 1 || max_pages < 1) return KDA_ERR_INVALID_ARG;
-  if (rank < 128 || rank > 512 || rank % 128 != 0 || (rope != 0 && rope != 64))
+  if (rank < 128 || rank > 512 || rank % 128 != 0 || (rope != 0 && rope != 64) || H > 65535)
     return KDA_ERR_UNSUPPORTED;
   if (!stride_ok(page_stride, dtype) || !stride_ok(row_stride, dtype) ||
       row_stride < rank + rope || page_stride < rank + rope)

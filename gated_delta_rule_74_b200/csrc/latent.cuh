@@ -17,7 +17,7 @@ struct LatentAppendShape {
   long long q_tok, q_head, qo_tok, qo_head;
   float eps;
   int interleaved;
-  int parts;                        // warps a token, set by the launcher
+  int parts;                        // warps a token, set by the launcher: 1, or the row's and the heads'
 };
 
 cudaError_t launch_latent_append(const void* kv, const float* w, const float* inv_freq,
@@ -42,7 +42,7 @@ __device__ __forceinline__ int cu_at(const int32_t* cu, int n, int T) {
 __device__ __forceinline__ bool token_sequence(long long tok, int N, int L, const int32_t* cu,
                                                int T, int lane, int* seq, int* first, int* count) {
   if (!cu) {
-    *seq = (int)(tok / L);
+    *seq = (int)((uint32_t)tok / (uint32_t)L);          // tokens are fewer than 2^31
     *first = *seq * L;
     *count = L;
     return true;

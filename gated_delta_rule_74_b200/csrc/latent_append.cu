@@ -10,12 +10,13 @@
 // bits (a far position has lost its angle in 32), the sine and cosine of the fraction in
 // 32.  Sums and products are fp32, rounded once to the cache's type.
 //
-// Bound by memory: every byte is read and written once.  One warp per (token, part):
-// part 0 is the token's own row (16 elements a lane, the norm a warp reduction), part
-// j > 0 the 16 query heads [16 (j - 1), 16 j).  Two heads a step, 16 lanes a head, each
-// lane two neighbouring pairs, so a warp reads whole 128-byte (bf16) runs; all of a
-// part's loads are issued before the first is used.  A part recomputes its token's
-// position and angles: a few dozen instructions against a wait for another warp.
+// Every byte is read and written once; what bounds the kernel short of memory is
+// instructions, so that a lane moves 16 bytes a load and store (a quarter of a bf16 head's
+// pairs, an eighth of an fp32 head's) and forms one frequency's angle, which the others
+// take from it.  With many tokens a warp does all of one, its row (16 elements a lane, the
+// norm a warp reduction) and its query heads, eight (fp32: four) a step, two steps'
+// loads ahead; with few (a decode step) a warp takes the row or 16 query heads, to wait
+// for fewer loads in a row.
 #include "kda_common.cuh"
 #include "latent.cuh"
 
@@ -25,47 +26,38 @@ namespace {
 constexpr int kRope = 64;               // rotated elements a row (or none)
 constexpr int kHeadsPerPart = 16;
 constexpr int kWarps = 4;
+constexpr uint32_t kAll = 0xffffffffu;
 
-struct Turn2 { float c0, s0, c1, s1; bool on; };   // two frequencies' cosines and sines
-
-template <typename T> struct Vec2;
-template <> struct Vec2<float> { using type = float2; };
-template <> struct Vec2<__nv_bfloat16> { using type = __nv_bfloat162; };
-
-__device__ __forceinline__ float2 up2(float2 v) { return v; }
-__device__ __forceinline__ float2 up2(__nv_bfloat162 v) { return __bfloat1622float2(v); }
-template <typename T> __device__ __forceinline__ typename Vec2<T>::type down2(float x, float y);
-template <> __device__ __forceinline__ float2 down2<float>(float x, float y) {
-  return make_float2(x, y);
-}
-template <> __device__ __forceinline__ __nv_bfloat162 down2<__nv_bfloat16>(float x, float y) {
-  return __floats2bfloat162_rn(x, y);
-}
-
-// The elements of pairs f, f + 1 (f = 2 j): (4j .. 4j+3) interleaved, else (2j, 2j+1) and
-// (32 + 2j, 32 + 2j + 1).
-template <typename T> struct Pairs { typename Vec2<T>::type u, w; };
-
-template <typename T>
-__device__ __forceinline__ Pairs<T> load_pairs(const T* x, int j, bool inter) {
-  using V = typename Vec2<T>::type;
-  return {*reinterpret_cast<const V*>(x + (inter ? 4 * j : 2 * j)),
-          *reinterpret_cast<const V*>(x + (inter ? 4 * j + 2 : kRope / 2 + 2 * j))};
-}
-template <typename T>
-__device__ __forceinline__ void store_turned(T* y, int j, bool inter, Pairs<T> p, const Turn2& t) {
-  using V = typename Vec2<T>::type;
-  if (t.on) {                                      // else a copy, bit for bit
-    const float2 u = up2(p.u), w = up2(p.w);
-    const float x0 = u.x, x1 = inter ? w.x : u.y, z0 = inter ? u.y : w.x, z1 = w.y;
-    const float a0 = x0 * t.c0 - z0 * t.s0, b0 = x0 * t.s0 + z0 * t.c0;
-    const float a1 = x1 * t.c1 - z1 * t.s1, b1 = x1 * t.s1 + z1 * t.c1;
-    p.u = inter ? down2<T>(a0, b0) : down2<T>(a0, a1);
-    p.w = inter ? down2<T>(a1, b1) : down2<T>(b0, b1);
+// E pairs of one lane (E: elements of 16 bytes): pairs [E j, E j + E), whose elements are
+// x[2 E j, 2 E j + 2 E) interleaved, else x[E j, ..) and x[32 + E j, ..).
+template <typename T> struct Pairs {
+  static constexpr int E = 16 / sizeof(T);
+  uint4 u, w;
+  __device__ void load(const T* x, int j, bool inter) {
+    u = *reinterpret_cast<const uint4*>(x + (inter ? 2 * E * j : E * j));
+    w = *reinterpret_cast<const uint4*>(x + (inter ? 2 * E * j + E : kRope / 2 + E * j));
   }
-  *reinterpret_cast<V*>(y + (inter ? 4 * j : 2 * j)) = p.u;
-  *reinterpret_cast<V*>(y + (inter ? 4 * j + 2 : kRope / 2 + 2 * j)) = p.w;
-}
+  __device__ void store(T* x, int j, bool inter) const {
+    *reinterpret_cast<uint4*>(x + (inter ? 2 * E * j : E * j)) = u;
+    *reinterpret_cast<uint4*>(x + (inter ? 2 * E * j + E : kRope / 2 + E * j)) = w;
+  }
+  __device__ void turn(const float (&c)[E], const float (&s)[E], bool inter) {
+    T a[E], b[E];                                     // the loads' elements
+    *reinterpret_cast<uint4*>(a) = u;
+    *reinterpret_cast<uint4*>(b) = w;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      // interleaved: pair i is elements 2 i, 2 i + 1 of the two loads together
+      T& p = inter ? (i < E / 2 ? a[(2 * i) % E] : b[(2 * i) % E]) : a[i];
+      T& q = inter ? (i < E / 2 ? a[(2 * i + 1) % E] : b[(2 * i + 1) % E]) : b[i];
+      const float x = to_f32(p), y = to_f32(q);
+      p = from_f32<T>(x * c[i] - y * s[i]);
+      q = from_f32<T>(x * s[i] + y * c[i]);
+    }
+    u = *reinterpret_cast<const uint4*>(a);
+    w = *reinterpret_cast<const uint4*>(b);
+  }
+};
 
 // cos and sin of pos * freq
 __device__ __forceinline__ void turn(int pos, float freq, float* c, float* s) {
@@ -74,79 +66,92 @@ __device__ __forceinline__ void turn(int pos, float freq, float* c, float* s) {
   sincospif(2.0f * (float)t, s, c);
 }
 
-template <typename T>
-__global__ void __launch_bounds__(32 * kWarps)
+template <typename T, bool kInter>
+__global__ void __launch_bounds__(32 * kWarps, 6)
 kda_latent_append_kernel(const T* __restrict__ kv, const float* __restrict__ w,
-                         const float* __restrict__ inv_freq, const T* __restrict__ q_pe,
-                         T* __restrict__ q_out, T* __restrict__ cache,
-                         const int32_t* __restrict__ page_table,
+                         const float* __restrict__ inv_freq, const T* q_pe, T* q_out,
+                         T* __restrict__ cache, const int32_t* __restrict__ page_table,
                          const int32_t* __restrict__ seq_lens,
                          const int32_t* __restrict__ cu_seqlens, LatentAppendShape sh) {
+  constexpr int E = 16 / sizeof(T);                   // elements of a 16-byte load
+  constexpr int NV = 16 / E;                          // a row's loads of a lane
+  constexpr int LH = 32 / E, HP = 32 / LH;            // lanes of a head, heads of a step
   const int lane = threadIdx.x & 31;
-  const long long unit = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const long long tok = unit / sh.parts;
-  const int part = (int)(unit - tok * sh.parts);
+  const int tok = blockIdx.x * kWarps + (threadIdx.x >> 5), part = blockIdx.y;
   if (tok >= sh.tokens) return;
 
-  // the token's own loads do not wait for its position
-  constexpr int E = 16 / sizeof(T);                   // elements of a 16-byte load
-  constexpr int NV = 16 / E;                          // loads of a lane: 16 elements at most
+  // ---- query heads [h0, h1), two steps' loads ahead; the loads do not wait for the position
+  const int j = lane % LH;
+  // (the row's own part of several has none)
+  const bool heads = q_pe && (sh.parts == 1 || part > 0);
+  const int h0 = (part > 0 ? (part - 1) * kHeadsPerPart : 0) + lane / LH;
+  const int h1 = !heads ? 0 : sh.parts == 1 ? sh.H : min(part * kHeadsPerPart, sh.H);
+  Pairs<T> p0, p1;
+  auto load_heads = [&](int h) {
+    if (h < h1) p0.load(q_pe + tok * sh.q_tok + h * sh.q_head, j, kInter);
+    if (h + HP < h1) p1.load(q_pe + tok * sh.q_tok + (h + HP) * sh.q_head, j, kInter);
+  };
+  load_heads(h0);
+  const T* const x = kv + tok * sh.kv_stride;
   uint4 xv[NV];
+  Pairs<T> rp;
   if (part == 0) {
-    const T* x = kv + tok * sh.kv_stride;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int e = (i * 32 + lane) * E;
       xv[i] = e < sh.rank ? __ldg(reinterpret_cast<const uint4*>(x + e)) : make_uint4(0, 0, 0, 0);
     }
+    if (sh.rope && lane < LH) rp.load(x + sh.rank, lane, kInter);
   }
-  int seq, i0, cnt;
-  if (!token_sequence(tok, sh.N, sh.L, cu_seqlens, (int)sh.tokens, lane, &seq, &i0, &cnt)) return;
-  const int pos = seq_lens[seq] - cnt + (int)(tok - i0);
+  int seq, first, cnt;
+  if (!token_sequence(tok, sh.N, sh.L, cu_seqlens, (int)sh.tokens, lane, &seq, &first, &cnt)) return;
+  const int pos = __ldg(seq_lens + seq) - cnt + (tok - first);
 
-  const int j = lane & 15;                            // pairs 2j, 2j + 1
-  Turn2 t = {1.f, 0.f, 1.f, 0.f, false};
-  if (sh.rope && inv_freq) {
-    const float2 f = __ldg(reinterpret_cast<const float2*>(inv_freq) + j);
-    turn(pos, f.x, &t.c0, &t.s0);
-    turn(pos, f.y, &t.c1, &t.s1);
-    t.on = true;
+  // the row's slot (page -1: outside of the table or the cache, it is not written)
+  int page = -1, row = 0;
+  if (part == 0 && pos >= 0) {
+    const int pg = pos / sh.page_size;
+    row = pos - pg * sh.page_size;
+    if (pg < sh.max_pages) page = __ldg(page_table + (long long)seq * sh.max_pages + pg);
   }
-
-  if (part > 0) {
-    const int h0 = (part - 1) * kHeadsPerPart + (lane >> 4);
-    Pairs<T> p[kHeadsPerPart / 2];
+  const bool turned = sh.rope && inv_freq;
+  float c[E], s[E];
+  if (turned) {
+    float cl, sl;                                     // of frequency `lane`
+    turn(pos, __ldg(inv_freq + lane), &cl, &sl);
 #pragma unroll
-    for (int i = 0; i < kHeadsPerPart / 2; ++i)
-      if (h0 + 2 * i < sh.H)
-        p[i] = load_pairs(q_pe + tok * sh.q_tok + (h0 + 2 * i) * sh.q_head, j, sh.interleaved);
-#pragma unroll
-    for (int i = 0; i < kHeadsPerPart / 2; ++i)
-      if (h0 + 2 * i < sh.H)
-        store_turned(q_out + tok * sh.qo_tok + (h0 + 2 * i) * sh.qo_head, j, sh.interleaved, p[i],
-                      t);
-    return;
+    for (int i = 0; i < E; ++i) {
+      c[i] = __shfl_sync(kAll, cl, E * j + i);
+      s[i] = __shfl_sync(kAll, sl, E * j + i);
+    }
   }
 
-  // the slot: outside the table or the cache, the row is not written
-  if (pos < 0 || pos / sh.page_size >= sh.max_pages) return;
-  const int page = __ldg(page_table + (long long)seq * sh.max_pages + pos / sh.page_size);
+  for (int h = h0; h < h1; h += 2 * HP) {
+    if (turned) p0.turn(c, s, kInter);
+    p0.store(q_out + tok * sh.qo_tok + h * sh.qo_head, j, kInter);
+    if (h + HP < h1) {
+      if (turned) p1.turn(c, s, kInter);
+      p1.store(q_out + tok * sh.qo_tok + (h + HP) * sh.qo_head, j, kInter);
+    }
+    load_heads(h + 2 * HP);
+  }
   if (page < 0 || page >= sh.num_pages) return;
-  T* y = cache + page * sh.page_stride + (pos % sh.page_size) * sh.row_stride;
 
+  // ---- the row
+  T* const y = cache + page * sh.page_stride + row * sh.row_stride;
   if (w) {
-    float x[16], ss = 0.f;
+    float f[16], ss = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const T* xe = reinterpret_cast<const T*>(&xv[i]);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        x[i * E + e] = to_f32(xe[e]);
-        ss = fmaf(x[i * E + e], x[i * E + e], ss);
+        f[i * E + e] = to_f32(xe[e]);
+        ss = fmaf(f[i * E + e], f[i * E + e], ss);
       }
     }
 #pragma unroll
-    for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(kAll, ss, o);
     const float r = rsqrtf(ss / (float)sh.rank + sh.eps);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -156,10 +161,10 @@ kda_latent_append_kernel(const T* __restrict__ kv, const float* __restrict__ w,
 #pragma unroll
       for (int e4 = 0; e4 < E; e4 += 4) {
         const float4 g = __ldg(reinterpret_cast<const float4*>(w + e0 + e4));
-        xe[e4] = from_f32<T>(x[i * E + e4] * r * g.x);
-        xe[e4 + 1] = from_f32<T>(x[i * E + e4 + 1] * r * g.y);
-        xe[e4 + 2] = from_f32<T>(x[i * E + e4 + 2] * r * g.z);
-        xe[e4 + 3] = from_f32<T>(x[i * E + e4 + 3] * r * g.w);
+        xe[e4] = from_f32<T>(f[i * E + e4] * r * g.x);
+        xe[e4 + 1] = from_f32<T>(f[i * E + e4 + 1] * r * g.y);
+        xe[e4 + 2] = from_f32<T>(f[i * E + e4 + 2] * r * g.z);
+        xe[e4 + 3] = from_f32<T>(f[i * E + e4 + 3] * r * g.w);
       }
     }
   }
@@ -168,10 +173,20 @@ kda_latent_append_kernel(const T* __restrict__ kv, const float* __restrict__ w,
     const int e = (i * 32 + lane) * E;
     if (e < sh.rank) *reinterpret_cast<uint4*>(y + e) = xv[i];
   }
-  if (sh.rope && lane < 16) {
-    const Pairs<T> p = load_pairs(kv + tok * sh.kv_stride + sh.rank, j, sh.interleaved);
-    store_turned(y + sh.rank, j, sh.interleaved, p, t);
+  if (sh.rope && lane < LH) {
+    if (turned) rp.turn(c, s, kInter);
+    rp.store(y + sh.rank, lane, kInter);
   }
+}
+
+template <typename T>
+void run_append(const void* kv, const float* w, const float* inv_freq, const void* q_pe,
+                void* q_out, void* cache, const int32_t* page_table, const int32_t* seq_lens,
+                const int32_t* cu_seqlens, const LatentAppendShape& sh, cudaStream_t stream) {
+  auto kern = sh.interleaved ? kda_latent_append_kernel<T, true> : kda_latent_append_kernel<T, false>;
+  kern<<<dim3((unsigned)((sh.tokens + kWarps - 1) / kWarps), sh.parts), 32 * kWarps, 0, stream>>>(
+      static_cast<const T*>(kv), w, inv_freq, static_cast<const T*>(q_pe), static_cast<T*>(q_out),
+      static_cast<T*>(cache), page_table, seq_lens, cu_seqlens, sh);
 }
 
 }  // namespace
@@ -181,21 +196,13 @@ cudaError_t launch_latent_append(const void* kv, const float* w, const float* in
                                  const int32_t* page_table, const int32_t* seq_lens,
                                  const int32_t* cu_seqlens, LatentAppendShape sh, int dtype,
                                  cudaStream_t stream) {
-  sh.parts = 1 + (q_pe ? (sh.H + kHeadsPerPart - 1) / kHeadsPerPart : 0);
-  const long long units = sh.tokens * sh.parts;
-  const unsigned grid = (unsigned)((units + kWarps - 1) / kWarps);
-  if (dtype == KDA_BF16)
-    KDA_TIMED(KDA_KERNEL_LATENT_APPEND, stream,
-              kda_latent_append_kernel<<<grid, 32 * kWarps, 0, stream>>>(
-                  static_cast<const __nv_bfloat16*>(kv), w, inv_freq,
-                  static_cast<const __nv_bfloat16*>(q_pe), static_cast<__nv_bfloat16*>(q_out),
-                  static_cast<__nv_bfloat16*>(cache), page_table, seq_lens, cu_seqlens, sh));
-  else
-    KDA_TIMED(KDA_KERNEL_LATENT_APPEND, stream,
-              kda_latent_append_kernel<<<grid, 32 * kWarps, 0, stream>>>(
-                  static_cast<const float*>(kv), w, inv_freq, static_cast<const float*>(q_pe),
-                  static_cast<float*>(q_out), static_cast<float*>(cache), page_table, seq_lens,
-                  cu_seqlens, sh));
+  int sms = 0;
+  if (!device_ctx(&sms, nullptr)) return cudaErrorInvalidDevice;
+  // a warp a token once there are 16 warps an SM of them
+  sh.parts = !q_pe || sh.tokens >= 16LL * sms ? 1 : 1 + (sh.H + kHeadsPerPart - 1) / kHeadsPerPart;
+  auto run = dtype == KDA_BF16 ? run_append<__nv_bfloat16> : run_append<float>;
+  KDA_TIMED(KDA_KERNEL_LATENT_APPEND, stream,
+            run(kv, w, inv_freq, q_pe, q_out, cache, page_table, seq_lens, cu_seqlens, sh, stream));
   note_launches(1);
   return cudaGetLastError();
 }

@@ -300,6 +300,15 @@ def test_append_packed(N):
     append_close(x, *run_append(x, False), False)
 
 
+@pytest.mark.parametrize("dtype,inter,H", [("bf16", False, 12), ("bf16", True, 9), ("f32", False, 5),
+                                           ("f32", True, 33)])
+def test_append_many_tokens(dtype, inter, H):
+    """Enough tokens that a warp takes a whole one."""
+    cu = [0, 1000, 1001, 1001, 2700]
+    x = make_append(dtype, [1300, 90, 5, 1699], 2705, H, 128, 64, 64, True, cu=cu)
+    append_close(x, *run_append(x, inter), inter)
+
+
 def test_append_far_positions():
     """Angles of positions in the millions: a 32-bit product would be off by a tenth."""
     lens = [5_000_003, 2 ** 30 + 7]
