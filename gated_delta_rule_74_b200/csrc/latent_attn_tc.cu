@@ -97,7 +97,7 @@ TcPlan tc_plan(int nr, int rank, int rope, int page_size) {
 
 struct TcBars {
   uint64_t q_full[2], q_empty[2];
-  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t full[kMaxStages], empty[kMaxStages][2];      // empty: by pair of the stage
   uint64_t rope_empty[2];
   uint64_t s_full[2], s_empty;
   uint64_t p_full[2], pv_done[2];
@@ -131,7 +131,7 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
   __shared__ TcBars bar;
   __shared__ LatentStart st;
   __shared__ long long s_sum[33];
-  __shared__ float2 s_m2[NR / 2];                   // maxima the weights refer to, scaled
+  __shared__ float s_m[NR];                         // maxima the weights refer to, scaled
   __shared__ uint8_t s_more[NR];                    // tokens each row sees more than the first
   __shared__ float s_row[NR];                       // rescaling factors, then 1 / sum
   __shared__ float s_red[4][NR];                    // the lane quarters' maxima, then sums
@@ -140,7 +140,6 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
   constexpr int nr = NR, kSBuf = NR <= 80 ? 2 : 1;
   constexpr uint32_t kTmemS = 4 * NR;
   const int npair = pl.npair;
-  float* const s_m = reinterpret_cast<float*>(s_m2);
   const uint32_t stage_bytes = pl.spair * kPair;
   uint8_t* const sq = sm;
   uint8_t* const sst = sq + pl.nq * pl.q_bytes;
@@ -162,7 +161,8 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
     }
     for (int i = 0; i < kMaxStages; ++i) {
       mbar_init(&bar.full[i], 2);                   // warps 0 and 2
-      mbar_init(&bar.empty[i], 1);
+      mbar_init(&bar.empty[i][0], 1);
+      mbar_init(&bar.empty[i][1], 1);
     }
     mbar_init(&bar.s_empty, kSoft / 32);
     mbar_init(&bar.o_empty, kSoft / 32);
@@ -202,7 +202,7 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
         const int page = next_page, row = (t * kTcTile + lane * pl.box_rows) % sh.page_size;
         next_page = look(t + 1);
         for (int s = 0; s < pl.ns; ++s) {
-          if (use > 0) ok = __all_sync(kAll, mbar_wait(&bar.empty[stage], (use - 1) & 1, kWaitLimit));
+          if (use > 0) ok = __all_sync(kAll, mbar_wait(&bar.empty[stage][w], (use - 1) & 1, kWaitLimit));
           const bool with_rope = rope && w == 1 && s == 0;
           if (with_rope && ruse > 0)
             ok = ok && __all_sync(kAll, mbar_wait(&bar.rope_empty[rs], (ruse - 1) & 1, kWaitLimit));
@@ -279,6 +279,7 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
     const uint64_t dv = desc_mnmajor_sw128(smem_u32(sst), kTcTile, 0);
     const uint64_t dp = desc_mnmajor_sw32(smem_u32(sp), kTcTile, 0);
     const uint32_t block = (uint32_t)(nr * 8);            // 64 columns of Q, in 16 bytes
+    const int early = min(pl.ns, pl.stages - pl.ns);      // stages of scores ahead of the values
     LatentWalk walk(st);
     LatentPiece p;
     uint32_t it = 0, g = 0;                              // blocks, tiles
@@ -339,8 +340,12 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
         if (i > 0) {
           const uint32_t pb = pl.np == 2 ? g & 1 : 0, ppar = (pl.np == 2 ? g >> 1 : g) & 1;
           uint32_t polls = 0;
+          while (ok && (!scores || s >= early)) {        // nothing else can be done before
+            ok = __all_sync(kAll, mbar_wait(&bar.p_full[pb], ppar, kWaitLimit));
+            break;
+          }
           while (ok && !__all_sync(kAll, mbar_test_wait(&bar.p_full[pb], ppar))) {
-            if (scores && s < pl.ns && (kSBuf == 2 || s > 0 || s_free(ts)) &&
+            if (scores && s < early && (kSBuf == 2 || s > 0 || s_free(ts)) &&
                 __all_sync(kAll, mbar_test_wait(&bar.full[stage], use & 1)))
               issue_qk(s++, ts, q0);
             if (++polls > kPollLimit) ok = false;
@@ -358,13 +363,14 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
               mma_ss_all(d, a, b, id_pv, i > 1);
 #pragma unroll
               for (int kk = 1; kk < 4; ++kk) mma_ss_all(d, a + 128 * kk, b + 32 * kk, id_pv, 1);
+              mma_commit(&bar.empty[vstage][0]);
               if (two) {
                 mma_ss_all(d + nr, a + kPair / 16, b, id_pv, i > 1);
 #pragma unroll
                 for (int kk = 1; kk < 4; ++kk)
                   mma_ss_all(d + nr, a + kPair / 16 + 128 * kk, b + 32 * kk, id_pv, 1);
               }
-              mma_commit(&bar.empty[vstage]);
+              mma_commit(&bar.empty[vstage][1]);
               if (v == pl.ns - 1) mma_commit(&bar.pv_done[pb]);
             }
             __syncwarp();
@@ -423,10 +429,14 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
         s_m[ts] = ts < p.rows ? kNone : INFINITY;
         s_more[ts] = (uint8_t)((p.row_in_seq + ts) / sh.H - p.row_in_seq / sh.H);
       }
-      float l[kG][2];
-#pragma unroll
-      for (int i = 0; i < kG; ++i) l[i][0] = l[i][1] = 0.f;
+      float l[kG][2], m[kG][2];                          // of this thread's rows
       named_bar(1, kSoft);
+#pragma unroll
+      for (int i = 0; i < kG; ++i) {
+        l[i][0] = l[i][1] = 0.f;
+        m[i][0] = i < ng ? s_m[8 * (g0 + i) + c0] : INFINITY;
+        m[i][1] = i < ng ? s_m[8 * (g0 + i) + c0 + 1] : INFINITY;
+      }
       for (int t = p.t0; t < p.t1; ++t, ++g) {
         const uint32_t sb = kSBuf == 2 ? g & 1 : 0;
         ok = ok && mbar_wait(&bar.s_full[sb], (kSBuf == 2 ? g >> 1 : g) & 1, kWaitLimit);
@@ -442,24 +452,25 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar.s_empty);
         }
-        // x = scaled score less the maximum, in place; whether some x passes 2^8
+        // whether some scaled score passes its row's maximum by 2^8
         float top = -INFINITY;
-        auto less_max = [&](bool first_time) {
+        if (mixed) {
 #pragma unroll
           for (int i = 0; i < kG; ++i)
             if (i < ng) {
-              const float2 m = s_m2[4 * (g0 + i) + (lane & 3)];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                if (first_time && mixed &&
-                    t * kTcTile + tok + 8 * (e >> 1) >=
-                        low + s_more[8 * (g0 + i) + c0 + (e & 1)])
+              for (int e = 0; e < 4; ++e)
+                if (t * kTcTile + tok + 8 * (e >> 1) >= low + s_more[8 * (g0 + i) + c0 + (e & 1)])
                   s[i][e] = 0xff800000u;                 // -inf
-                top = fmaxf(top, fmaf(__uint_as_float(s[i][e]), c, -(e & 1 ? m.y : m.x)));
-              }
             }
-        };
-        less_max(true);
+        }
+#pragma unroll
+        for (int i = 0; i < kG; ++i)
+          if (i < ng) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              top = fmaxf(top, fmaf(__uint_as_float(s[i][e]), c, -m[i][e & 1]));
+          }
         // rows that some query row does not see: nothing that 0 * would turn into a NaN
         if (mixed) {
           const int first = max(low - t * kTcTile, 0), per = sh.rank / 8;
@@ -501,8 +512,11 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
 #pragma unroll
           for (int i = 0; i < kG; ++i)
             if (i < ng) {
-              l[i][0] *= s_row[8 * (g0 + i) + c0];
-              l[i][1] *= s_row[8 * (g0 + i) + c0 + 1];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                l[i][e] *= s_row[8 * (g0 + i) + c0 + e];
+                m[i][e] = s_m[8 * (g0 + i) + c0 + e];
+              }
             }
           if (t > p.t0) {
             tc_fence_after();
@@ -522,22 +536,30 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
           }
         }
         if (puse > 0) ok = ok && pv_wait(pl.np);         // the buffer's last values are done
-        uint8_t* const pr = sp + pb * pl.p_bytes;
+        uint32_t pk[kG][2];                              // rows c0, c0 + 1 of tokens tok, tok + 8
 #pragma unroll
-        for (int i = 0; i < kG; ++i)
-          if (i < ng) {
-            const float2 m = s_m2[4 * (g0 + i) + (lane & 3)];
-            float x[4];
+        for (int i = 0; i < kG; ++i) {
+          float x[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              x[e] = ex2(fmaf(__uint_as_float(s[i][e]), c, -(e & 1 ? m.y : m.x)));
-            l[i][0] += x[0] + x[2];
-            l[i][1] += x[1] + x[3];
-            const uint32_t n = 8 * (g0 + i) + c0;
-            *reinterpret_cast<uint32_t*>(pr + off_mnmajor_sw32(n, tok, kTcTile)) = pack_bf16(x[0], x[1]);
-            *reinterpret_cast<uint32_t*>(pr + off_mnmajor_sw32(n, tok + 8, kTcTile)) =
-                pack_bf16(x[2], x[3]);
-          }
+          for (int e = 0; e < 4; ++e)
+            x[e] = i < ng ? ex2(fmaf(__uint_as_float(s[i][e]), c, -m[i][e & 1])) : 0.f;
+          l[i][0] += x[0] + x[2];
+          l[i][1] += x[1] + x[3];
+          pk[i][0] = pack_bf16(x[0], x[1]);
+          pk[i][1] = pack_bf16(x[2], x[3]);
+        }
+        // to shared memory two groups of rows at once: lane 8 k + j addresses row j of matrix k,
+        // tokens [8 (k % 2), + 8) of group i + k / 2
+        const uint32_t pr = smem_u32(sp + pb * pl.p_bytes);
+        const uint32_t at = 16 * wq + (lane & 15);
+#pragma unroll
+        for (int i = 0; i < kG; i += 2) {
+          if (i + 1 < ng)
+            stmatrix_x4(pr + chunk_mnmajor_sw32(g0 + i + (lane >> 4), at, kTcTile), pk[i][0],
+                        pk[i][1], pk[i + 1 < kG ? i + 1 : i][0], pk[i + 1 < kG ? i + 1 : i][1]);
+          else if (i < ng)
+            stmatrix_x2(pr + chunk_mnmajor_sw32(g0 + i, at, kTcTile), pk[i][0], pk[i][1]);
+        }
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.p_full[pb]);

@@ -187,6 +187,20 @@ __device__ __forceinline__ bool named_bar_or(uint32_t id, uint32_t nthreads, boo
   return r != 0;
 }
 
+// Store 8 x 8 matrices of 16-bit elements: in r[k] thread i holds row i / 4, columns
+// 2 (i % 4) + {0, 1} of matrix k, whose row j goes to the address given by lane 8 k + j.
+__device__ __forceinline__ void stmatrix_x4(uint32_t saddr, uint32_t r0, uint32_t r1, uint32_t r2,
+                                            uint32_t r3) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(saddr),
+               "r"(r0), "r"(r1), "r"(r2), "r"(r3)
+               : "memory");
+}
+__device__ __forceinline__ void stmatrix_x2(uint32_t saddr, uint32_t r0, uint32_t r1) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x2.shared.b16 [%0], {%1, %2};" ::"r"(saddr), "r"(r0),
+               "r"(r1)
+               : "memory");
+}
+
 // ------------------------------------------- programmatic dependent launch
 // Kernels of one call that follow each other on a stream may be launched with
 // programmatic stream serialization: the next grid can start before this one
