@@ -7,11 +7,13 @@
 // in one pass over the cache with the running maximum and sum of the softmax.  A row that
 // sees nothing gives zeros and a log-sum of -inf.
 //
-// One CTA holds 16 rows; a tile of 32 cached rows is brought to shared memory as fp32 once
-// and used for both products by all 16.  Scores: thread (r, j) takes row r against tokens
-// j and j + 16.  Output: thread d holds columns d and d + 256 of all 16 rows in registers.
-// Bound by shared-memory reads (each FMA's operands come from there), not by the cache's
-// bytes; fp32 has no tensor-core form of fp32 accuracy.
+// One CTA holds 16 rows; tiles of 32 cached rows come by cp.async into two buffers, the next
+// one under the arithmetic of this one, and each is used for both products by all 16 rows.
+// Scores: each of the eight warps takes an eighth of the columns of all 16 x 32, a thread
+// four rows by four tokens (eight 16-byte reads of shared memory for 64 FMAs); the eight
+// partial sums meet in shared memory.  Output: a thread holds eight rows by rank / 128
+// columns in registers (three reads for 8 rank / 128 FMAs).  Bound by the FMAs and these
+// reads, not by the cache's bytes: fp32 has no tensor-core form of fp32 accuracy.
 #include "latent_attn.cuh"
 #include "sm100.cuh"
 
@@ -23,92 +25,149 @@ constexpr int kRows = 16;                // rows of a block
 constexpr int kTile = 32;                // cached rows of a tile
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// One piece's results, straight to the output or to partial slot `slot` (>= 0).
-template <typename T>
-__device__ __forceinline__ void put(T* out, float* lse, const LatentPartials& pt, int slot,
-                                    int rank, long long row, int r, int nr, int d, float v) {
-  if (slot < 0) out[row * rank + d] = from_f32<T>(v);
-  else pt.o[((long long)slot * nr + r) * rank + d] = v;
+// Four neighbouring elements as fp32.
+__device__ __forceinline__ float4 four(const float* x) { return *reinterpret_cast<const float4*>(x); }
+__device__ __forceinline__ float4 four(const __nv_bfloat16* x) {
+  const uint2 u = *reinterpret_cast<const uint2*>(x);
+  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
+                     __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
+}
+// kD neighbouring elements as fp32; the first one's index is a multiple of kD.
+template <int kD, typename T>
+__device__ __forceinline__ void load_few(const T* x, float (&v)[kD]) {
+  if constexpr (kD == 4) {
+    const float4 f = four(x);
+    v[0] = f.x;
+    v[1] = f.y;
+    v[2] = f.z;
+    v[3] = f.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < kD; ++i) v[i] = to_f32(x[i]);
+  }
 }
 
-template <typename T>
+// Shared memory: Q [16][LD], two tiles [32][LD] (LD = D + 16 bytes: rows shift by four banks),
+// the warps' partial scores.
+template <typename T> __host__ __device__ constexpr int simt_ld(int D) { return D + 16 / (int)sizeof(T); }
+template <typename T> int simt_smem(int D) {
+  return (kRows + 2 * kTile) * simt_ld<T>(D) * (int)sizeof(T) + 8 * kRows * kTile * 4;
+}
+
+// kD: value columns of a thread, rank / 128
+template <typename T, int kD>
 __global__ void __launch_bounds__(kNT)
 kda_latent_simt_kernel(const T* __restrict__ q, const T* __restrict__ cache,
                        const int32_t* __restrict__ page_table,
                        const int32_t* __restrict__ seq_lens,
                        const int32_t* __restrict__ cu_seqlens, T* __restrict__ out,
                        float* __restrict__ lse, LatentAttnShape sh, LatentPartials pt) {
+  using namespace sm100;
   extern __shared__ float4 smem4[];
-  const int D = sh.rank + sh.rope, LD = D + 4;
-  float* const sq = reinterpret_cast<float*>(smem4);       // [16][LD]
-  float* const sk = sq + kRows * LD;                       // [32][LD]
-  __shared__ float sp[kTile][kRows];
-  __shared__ float s_alpha[kRows], s_l[kRows];
+  const int D = sh.rank + sh.rope, LD = simt_ld<T>(D);
+  T* const sq = reinterpret_cast<T*>(smem4);
+  T* const sk = sq + kRows * LD;
+  float* const sred = reinterpret_cast<float*>(sk + 2 * kTile * LD);   // [8][16][32]
+  __shared__ __align__(16) float sp[kTile][kRows];
+  __shared__ __align__(16) float s_alpha[kRows];
+  __shared__ float s_inv[kRows];
   __shared__ LatentStart st;
   __shared__ long long s_sum[33];
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   latent_find_start(sh, seq_lens, cu_seqlens, kRows, kTile, &st, s_sum);
   if (tid == 0) pt.head[blockIdx.x] = make_int4(0, 0, 0, 0);
 
-  const int r = tid >> 4, j0 = tid & 15;
   constexpr int E = 16 / sizeof(T);
+  const int DE = D / E;                                     // 16-byte pieces of a row
+  const int r = tid >> 4, j0 = tid & 15;                    // softmax: row r, tokens j0, j0 + 16
+  const int rg = lane >> 3, tg = lane & 7, D8 = D / 8;      // scores: rows rg + 4 a, tokens tg + 8 b
+  const int hr = 8 * (tid & 1), d0 = (tid >> 1) * kD;       // output: rows hr .., columns d0 ..
   LatentWalk walk(st);
   LatentPiece p;
   while (walk.next(sh, seq_lens, cu_seqlens, kRows, kTile, &p)) {
-    __syncthreads();
-    for (int i = tid; i < kRows * (D / E); i += kNT) {
-      const int row = i / (D / E), e = (i - row * (D / E)) * E;
-      uint4 u = make_uint4(0, 0, 0, 0);
-      if (row < p.rows) u = __ldg(reinterpret_cast<const uint4*>(q + (p.row0 + row) * D + e));
-      const T* x = reinterpret_cast<const T*>(&u);
-#pragma unroll
-      for (int k = 0; k < E; ++k) sq[row * LD + e + k] = to_f32(x[k]);
+    // tile t into buffer b; zeros where there is no row
+    auto fetch = [&](int t, int b) {
+      for (int i = tid; i < kTile * DE; i += kNT) {
+        const int row = i / DE, e = (i - row * DE) * E;
+        const int pos = t * kTile + row;
+        const T* src = cache;
+        uint32_t bytes = 0;
+        if (pos < p.len) {
+          const int pg = pos / sh.page_size;
+          const int page = __ldg(page_table + (long long)p.n * sh.max_pages + pg);
+          if (page >= 0 && page < sh.num_pages) {
+            src = cache + page * sh.page_stride + (pos - pg * sh.page_size) * sh.row_stride + e;
+            bytes = 16;
+          }
+        }
+        cp_async16(sk + (b * kTile + row) * LD + e, src, bytes);
+      }
+      cp_async_commit();
+    };
+    __syncthreads();                                        // the block before is done with
+    for (int i = tid; i < kRows * DE; i += kNT) {
+      const int row = i / DE, e = (i - row * DE) * E;
+      cp_async16(sq + row * LD + e, q + (p.row0 + (row < p.rows ? row : 0)) * D + e,
+                 row < p.rows ? 16 : 0);
     }
-    float acc[2][kRows];
+    fetch(p.t0, 0);
+    float acc[8][kD];
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) acc[0][i] = acc[1][i] = 0.f;
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int k = 0; k < kD; ++k) acc[i][k] = 0.f;
     float m = -INFINITY, l = 0.f;
     const int lim = min(p.start + (p.row_in_seq + r) / sh.H + 1, p.len);
     const int low = p.start + p.row_in_seq / sh.H + 1;      // the block's first row's limit
     for (int t = p.t0; t < p.t1; ++t) {
-      const int k0 = t * kTile;
-      __syncthreads();                                      // the tile before is consumed
-      for (int i = tid; i < kTile * (D / E); i += kNT) {
-        const int row = i / (D / E), e = (i - row * (D / E)) * E;
-        const int pos = k0 + row;
-        uint4 u = make_uint4(0, 0, 0, 0);
-        if (pos < p.len) {
-          const int page = __ldg(page_table + (long long)p.n * sh.max_pages + pos / sh.page_size);
-          if (page >= 0 && page < sh.num_pages)
-            u = __ldg(reinterpret_cast<const uint4*>(
-                cache + page * sh.page_stride + (pos % sh.page_size) * sh.row_stride + e));
-        }
-        const T* x = reinterpret_cast<const T*>(&u);
+      const int k0 = t * kTile, b = (t - p.t0) & 1;
+      if (t + 1 < p.t1) {
+        fetch(t + 1, b ^ 1);
+        cp_async_wait_group<1>();
+      } else {
+        cp_async_wait_group<0>();
+      }
+      __syncthreads();                                      // this tile is there
+      {
+        float x[4][4] = {};
+        const T* a = sq + rg * LD + warp * D8;
+        const T* y = sk + (b * kTile + tg) * LD + warp * D8;
+#pragma unroll 2
+        for (int d = 0; d < D8; d += 4) {
+          float4 av[4], yv[4];
 #pragma unroll
-        for (int k = 0; k < E; ++k) sk[row * LD + e + k] = to_f32(x[k]);
+          for (int i = 0; i < 4; ++i) {
+            av[i] = four(a + 4 * i * LD + d);
+            yv[i] = four(y + 8 * i * LD + d);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              x[i][j] = fmaf(av[i].x, yv[j].x, fmaf(av[i].y, yv[j].y,
+                        fmaf(av[i].z, yv[j].z, fmaf(av[i].w, yv[j].w, x[i][j]))));
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            sred[(warp * kRows + rg + 4 * i) * kTile + tg + 8 * j] = x[i][j];
       }
       __syncthreads();
       float s0 = 0.f, s1 = 0.f;
-      {
-        const float4* a = reinterpret_cast<const float4*>(sq + r * LD);
-        const float4* b0 = reinterpret_cast<const float4*>(sk + j0 * LD);
-        const float4* b1 = reinterpret_cast<const float4*>(sk + (j0 + 16) * LD);
-#pragma unroll 4
-        for (int i = 0; i < D / 4; ++i) {
-          const float4 x = a[i], y = b0[i], z = b1[i];
-          s0 = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, s0))));
-          s1 = fmaf(x.x, z.x, fmaf(x.y, z.y, fmaf(x.z, z.z, fmaf(x.w, z.w, s1))));
-        }
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        s0 += sred[(w * kRows + r) * kTile + j0];
+        s1 += sred[(w * kRows + r) * kTile + j0 + 16];
       }
       const float c = sh.scale * kLog2e;
       s0 = k0 + j0 < lim ? s0 * c : -INFINITY;
       s1 = k0 + j0 + 16 < lim ? s1 * c : -INFINITY;
       float mx = fmaxf(s0, s1);
-      bool nan = s0 != s0 || s1 != s1;                      // fmaxf drops a NaN: kept apart
 #pragma unroll
       for (int o = 8; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o, 16));
       const float mn = fmaxf(m, mx), ms = mn == -INFINITY ? 0.f : mn;
-      const float p0 = nan ? s0 + s1 : exp2f(s0 - ms), p1 = exp2f(s1 - ms);
+      const float p0 = exp2f(s0 - ms), p1 = exp2f(s1 - ms);   // a NaN score gives a NaN weight
       float ls = p0 + p1;
 #pragma unroll
       for (int o = 8; o; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o, 16);
@@ -121,38 +180,29 @@ kda_latent_simt_kernel(const T* __restrict__ q, const T* __restrict__ cache,
       __syncthreads();
       const bool mixed = k0 + kTile > low;                  // some row does not see some token
 #pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        acc[0][i] *= s_alpha[i];
-        acc[1][i] *= s_alpha[i];
-      }
-#pragma unroll 2
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int k = 0; k < kD; ++k) acc[i][k] *= s_alpha[hr + i];
+      const T* v0 = sk + b * kTile * LD + d0;
+#pragma unroll 4
       for (int j = 0; j < kTile; ++j) {
-        float w[kRows];
+        float v[kD], w[8];
+        load_few<kD>(v0 + j * LD, v);
+        *reinterpret_cast<float4*>(w) = *reinterpret_cast<const float4*>(&sp[j][hr]);
+        *reinterpret_cast<float4*>(w + 4) = *reinterpret_cast<const float4*>(&sp[j][hr + 4]);
 #pragma unroll
-        for (int i = 0; i < kRows; i += 4)
-          *reinterpret_cast<float4*>(w + i) = *reinterpret_cast<const float4*>(&sp[j][i]);
-        const float v0 = tid < sh.rank ? sk[j * LD + tid] : 0.f;
-        const float v1 = tid + kNT < sh.rank ? sk[j * LD + tid + kNT] : 0.f;
-        if (mixed) {                                        // a weight of zero takes nothing, not 0 * inf
+        for (int i = 0; i < 8; ++i)
 #pragma unroll
-          for (int i = 0; i < kRows; ++i) {
-            acc[0][i] = w[i] == 0.f ? acc[0][i] : fmaf(w[i], v0, acc[0][i]);
-            acc[1][i] = w[i] == 0.f ? acc[1][i] : fmaf(w[i], v1, acc[1][i]);
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < kRows; ++i) {
-            acc[0][i] = fmaf(w[i], v0, acc[0][i]);
-            acc[1][i] = fmaf(w[i], v1, acc[1][i]);
-          }
-        }
+          for (int k = 0; k < kD; ++k)                      // a weight of zero takes nothing, not 0 * inf
+            acc[i][k] = mixed && w[i] == 0.f ? acc[i][k] : fmaf(w[i], v[k], acc[i][k]);
       }
+      __syncthreads();                                      // the tile and its weights are used
     }
     // ---- results: whole blocks to the output, shared ones to a partial slot
     const bool first = p.t0 == 0, last = p.t1 == p.tiles;
     const int slot = first && last ? -1 : 2 * (int)blockIdx.x + (first ? 1 : 0);
     if (j0 == 0) {
-      s_l[r] = l;
+      s_inv[r] = l == 0.f ? 0.f : 1.0f / l;
       const float z = l == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m) * kLn2 + logf(l);
       if (slot >= 0) pt.lse[slot * kRows + r] = z;
       else if (lse && r < p.rows) lse[p.row0 + r] = z;
@@ -162,14 +212,13 @@ kda_latent_simt_kernel(const T* __restrict__ q, const T* __restrict__ cache,
           make_int4((int)p.row0, p.rows, latent_cta_of(p.pos + p.tiles - 1, st.W, st.G), 0);
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      if (i >= p.rows) break;
-      const float inv = s_l[i] == 0.f ? 0.f : 1.0f / s_l[i];
+    for (int i = 0; i < 8; ++i) {
+      if (hr + i >= p.rows) break;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int d = tid + h * kNT;
-        if (d < sh.rank)
-          put(out, lse, pt, slot, sh.rank, p.row0 + i, i, kRows, d, acc[h][i] * inv);
+      for (int k = 0; k < kD; ++k) {
+        const float o = acc[i][k] * s_inv[hr + i];
+        if (slot < 0) out[(p.row0 + hr + i) * sh.rank + d0 + k] = from_f32<T>(o);
+        else pt.o[((long long)slot * kRows + hr + i) * sh.rank + d0 + k] = o;
       }
     }
   }
@@ -202,53 +251,40 @@ __device__ __forceinline__ void join_add(float4& a, float w, const float4& v) {
   a.w = fmaf(w, v.w, a.w);
 }
 
+// Many items: block (c, y) takes rows y, y + gridDim.y, .. (or fours of rows) of the shared block
+// that starts in CTA c, if one does.  Few (`list`): the blocks that there are get listed and
+// their rows spread over the grid.
 template <typename T>
 __global__ void __launch_bounds__(kJT)
 kda_latent_join_kernel(T* __restrict__ out, float* __restrict__ lse, LatentPartials pt, int G,
-                       int nr, int rank) {
-  __shared__ int s_off[kLatentMaxCtas + 1];
+                       int nr, int rank, bool list) {
   __shared__ float s_w[kLatentMaxCtas];
   __shared__ float4 s_part[3][128];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31;
   const int g = tid >> 7, d4 = tid & 127;
+  __shared__ int s_list[kLatentMaxCtas], s_n;
+  __shared__ uint32_t s_mask[kLatentMaxCtas / 32];
+  int c0 = blockIdx.x;
   sm100::grid_dep_wait();
-  // units (rows, or four rows) of the CTAs' shared blocks before each CTA
-  if (warp == 0) {
-    int run = 0;
-    for (int c0 = 0; c0 < G; c0 += 32) {
-      const int c = c0 + lane;
-      int v = 0;
-      if (c < G) {
-        const int4 hd = pt.head[c];
-        v = hd.z - c + 1 <= kFew ? (hd.y + 3) / 4 : hd.y;
-      }
-      int s = v;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int up = __shfl_up_sync(0xffffffffu, s, o);
-        if (lane >= o) s += up;
-      }
-      if (c < G) s_off[c] = run + s - v;
-      run += __shfl_sync(0xffffffffu, s, 31);
+  if (list) {                                          // in the CTAs' order: every block's is the same
+    for (int c = tid; c - lane < G; c += kJT) {
+      const uint32_t some = __ballot_sync(0xffffffffu, c < G && pt.head[c].y > 0);
+      if (lane == 0) s_mask[c >> 5] = some;
     }
-    if (lane == 0) s_off[G] = run;
+    __syncthreads();
+    for (int c = tid; c - lane < G; c += kJT) {
+      const uint32_t some = s_mask[c >> 5];
+      int at = __popc(some & ((1u << lane) - 1));
+      for (int w = 0; w < c >> 5; ++w) at += __popc(s_mask[w]);
+      if (some >> lane & 1) s_list[at] = c;
+      if (c == G - 1) s_n = at + (int)(some >> lane & 1);
+    }
+    __syncthreads();
   }
-  __syncthreads();
-  const int units = s_off[G];
-  for (int u = blockIdx.x; u < units; u += gridDim.x) {
-    int lo = 0, hi = G - 1;                            // the last CTA that starts at or before u
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) / 2;
-      if (s_off[mid] <= u) lo = mid;
-      else hi = mid - 1;
-    }
-    const int c0 = lo;
-    const int4 hd = pt.head[c0];
-    const int k = hd.z - c0 + 1;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (k <= kFew) {
-      const int r = 4 * (u - s_off[c0]) + g;
-      if (r >= hd.y) continue;
+  int4 hd = list ? make_int4(0, 0, 0, 0) : pt.head[c0];
+  int k = hd.z - c0 + 1;
+  if (!list && k <= kFew) {
+    for (int r = 4 * blockIdx.y + g; r < hd.y; r += 4 * gridDim.y) {
       float w[kFew];
       float4 v[kFew];
 #pragma unroll
@@ -269,14 +305,26 @@ kda_latent_join_kernel(T* __restrict__ out, float* __restrict__ lse, LatentParti
       const float inv = z == 0.f ? 0.f : 1.0f / z;
       if (d4 == 0 && lse) lse[hd.x + r] = z == 0.f ? -INFINITY : Ms + logf(z);
       if (d4 * 4 < rank) {
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < kFew; ++i)
           if (i < k) join_add(a, expf(w[i] - Ms) * inv, v[i]);
         join_store(out + (long long)(hd.x + r) * rank + d4 * 4, a);
       }
-      continue;
     }
-    const int r = u - s_off[c0];
+    return;
+  }
+  const int u0 = list ? blockIdx.x : blockIdx.y, du = list ? gridDim.x : gridDim.y;
+  const int units = list ? s_n * nr : hd.y;
+  for (int u = u0; u < units; u += du) {
+    int r = u;
+    if (list) {
+      c0 = s_list[u / nr];
+      r = u % nr;
+      hd = pt.head[c0];
+      k = hd.z - c0 + 1;
+      if (r >= hd.y) continue;
+    }
     __syncthreads();                                   // s_w and s_part of the row before are read
     for (int i = tid; i < k; i += kJT) s_w[i] = pt.lse[join_slot(c0, i) * nr + r];
     __syncthreads();
@@ -292,6 +340,7 @@ kda_latent_join_kernel(T* __restrict__ out, float* __restrict__ lse, LatentParti
     const float inv = z == 0.f ? 0.f : 1.0f / z;
     if (tid == 0 && lse) lse[hd.x + r] = z == 0.f ? -INFINITY : Ms + logf(z);
     const int i0 = k * g / 4, i1 = k * (g + 1) / 4;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
     if (d4 * 4 < rank) {
 #pragma unroll 8
       for (int i = i0; i < i1; ++i)
@@ -314,7 +363,24 @@ kda_latent_join_kernel(T* __restrict__ out, float* __restrict__ lse, LatentParti
   }
 }
 
-int simt_smem(int D) { return (kRows + kTile) * (D + 4) * 4; }
+template <typename T>
+using SimtKernel = void (*)(const T*, const T*, const int32_t*, const int32_t*, const int32_t*, T*,
+                            float*, LatentAttnShape, LatentPartials);
+template <typename T> SimtKernel<T> simt_kernel(int rank) {
+  switch (rank) {
+    case 128: return kda_latent_simt_kernel<T, 1>;
+    case 256: return kda_latent_simt_kernel<T, 2>;
+    case 384: return kda_latent_simt_kernel<T, 3>;
+    default: return kda_latent_simt_kernel<T, 4>;
+  }
+}
+template <typename T> bool simt_setup() {
+  for (int rank = 128; rank <= 512; rank += 128)
+    if (cudaFuncSetAttribute(simt_kernel<T>(rank), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             simt_smem<T>(rank + 64)) != cudaSuccess)
+      return false;
+  return true;
+}
 
 template <typename T>
 cudaError_t run_simt(const void* q, const void* cache, const int32_t* page_table,
@@ -322,13 +388,13 @@ cudaError_t run_simt(const void* q, const void* cache, const int32_t* page_table
                      const LatentAttnShape& sh, int G, const LatentPartials& pt,
                      cudaStream_t stream) {
   KDA_TIMED(KDA_KERNEL_LATENT_ATTN, stream,
-            kda_latent_simt_kernel<T><<<G, kNT, simt_smem(sh.rank + sh.rope), stream>>>(
+            simt_kernel<T>(sh.rank)<<<G, kNT, simt_smem<T>(sh.rank + sh.rope), stream>>>(
                 static_cast<const T*>(q), static_cast<const T*>(cache), page_table, seq_lens, cu,
                 static_cast<T*>(out), lse, sh, pt));
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   note_launches(1);
-  return launch_latent_join(out, lse, pt, G, kRows, sh.rank,
+  return launch_latent_join(out, lse, pt, G, kRows, sh.rank, latent_items(sh, kRows),
                             sizeof(T) == 2 ? KDA_BF16 : KDA_F32, stream);
 }
 
@@ -336,22 +402,27 @@ int simt_ctas(int sms) { return 2 * sms < kLatentMaxCtas ? 2 * sms : kLatentMaxC
 
 }  // namespace
 
-// Four join blocks an SM are resident; more would only wait.
+// `items`: blocks of rows of the call (packed: about).  Few of them are spread over the rows.
 cudaError_t launch_latent_join(void* out, float* lse, const LatentPartials& pt, int G, int nr,
-                               int rank, int dtype, cudaStream_t stream) {
-  int sms = 0;
-  if (!device_ctx(&sms, nullptr)) return cudaErrorInvalidDevice;
+                               int rank, long long items, int dtype, cudaStream_t stream) {
+  const bool list = items <= 16;
+  const dim3 grid = list ? dim3(2 * G) : dim3(G, (nr + 3) / 4);
   cudaError_t e = cudaSuccess;
   if (dtype == KDA_BF16)
     KDA_TIMED(KDA_KERNEL_LATENT_ATTN, stream,
-              e = launch_after(kda_latent_join_kernel<__nv_bfloat16>, dim3(4 * sms), dim3(kJT), 0,
-                               stream, static_cast<__nv_bfloat16*>(out), lse, pt, G, nr, rank));
+              e = launch_after(kda_latent_join_kernel<__nv_bfloat16>, grid, dim3(kJT), 0, stream,
+                               static_cast<__nv_bfloat16*>(out), lse, pt, G, nr, rank, list));
   else
     KDA_TIMED(KDA_KERNEL_LATENT_ATTN, stream,
-              e = launch_after(kda_latent_join_kernel<float>, dim3(4 * sms), dim3(kJT), 0, stream,
-                               static_cast<float*>(out), lse, pt, G, nr, rank));
+              e = launch_after(kda_latent_join_kernel<float>, grid, dim3(kJT), 0, stream,
+                               static_cast<float*>(out), lse, pt, G, nr, rank, list));
   note_launches(1);
   return e;
+}
+
+long long latent_items(const LatentAttnShape& sh, int nr) {
+  return sh.L > 0 ? sh.N * (((long long)sh.L * sh.H + nr - 1) / nr)
+                  : ((long long)sh.T * sh.H + nr - 1) / nr;
 }
 
 size_t latent_attn_scratch_bytes(int N, int L, int T, int H, int rank, int page_size, int dtype,
@@ -368,15 +439,8 @@ cudaError_t launch_latent_attn(const void* q, const void* cache, const int32_t* 
   int sms = 0;
   cudaMemPool_t pool = nullptr;
   if (!device_ctx(&sms, ws ? nullptr : &pool)) return cudaErrorInvalidDevice;
-  if (!once_per_device(kOnceLatentSimt, []() {
-        const int most = simt_smem(576);
-        return cudaFuncSetAttribute(kda_latent_simt_kernel<float>,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize, most) ==
-                   cudaSuccess &&
-               cudaFuncSetAttribute(kda_latent_simt_kernel<__nv_bfloat16>,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize, most) ==
-                   cudaSuccess;
-      }))
+  if (!once_per_device(kOnceLatentSimt,
+                       []() { return simt_setup<float>() && simt_setup<__nv_bfloat16>(); }))
     return cudaErrorInvalidDevice;
   const size_t bytes =
       latent_attn_scratch_bytes(sh.N, sh.L, sh.T, sh.H, sh.rank, sh.page_size, dtype, sms);

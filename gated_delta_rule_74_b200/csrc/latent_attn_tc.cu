@@ -133,7 +133,7 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
   __shared__ long long s_sum[33];
   __shared__ float s_m[NR];                         // maxima the weights refer to, scaled
   __shared__ uint8_t s_more[NR];                    // tokens each row sees more than the first
-  __shared__ float s_row[NR];                       // rescaling factors, then 1 / sum
+  __shared__ __align__(16) float s_row[NR];         // rescaling factors, then 1 / sum
   __shared__ float s_red[4][NR];                    // the lane quarters' maxima, then sums
   __shared__ uint32_t s_tmem;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -407,10 +407,9 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
     }
   } else {
     // ------------------------------------------------------------- softmax and results
-    constexpr int kGroups = NR / 8;                      // of eight rows; half = 0 takes the odd one
-    constexpr int kG = (kGroups + 1) / 2;
+    constexpr int kG = NR / 16;                          // groups of eight rows of a half
     const int wq = warp & 3, half = (warp - 4) >> 2, ts = tid - 128;
-    const int g0 = half * kG, ng = half ? kGroups - kG : kG;
+    const int g0 = half * kG;
     const int tok = 16 * wq + (lane >> 2), c0 = 2 * (lane & 3);   // tokens tok, tok + 8
     const uint32_t tl = tb + ((uint32_t)(32 * wq) << 16);
     const float c = sh.scale * kLog2e;
@@ -434,8 +433,8 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
 #pragma unroll
       for (int i = 0; i < kG; ++i) {
         l[i][0] = l[i][1] = 0.f;
-        m[i][0] = i < ng ? s_m[8 * (g0 + i) + c0] : INFINITY;
-        m[i][1] = i < ng ? s_m[8 * (g0 + i) + c0 + 1] : INFINITY;
+        m[i][0] = s_m[8 * (g0 + i) + c0];
+        m[i][1] = s_m[8 * (g0 + i) + c0 + 1];
       }
       for (int t = p.t0; t < p.t1; ++t, ++g) {
         const uint32_t sb = kSBuf == 2 ? g & 1 : 0;
@@ -445,7 +444,7 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
         uint32_t s[kG][4];
 #pragma unroll
         for (int i = 0; i < kG; ++i)
-          if (i < ng) tmem_ld_16x256b(tl + kTmemS + sb * nr + 8 * (g0 + i), s[i]);
+          tmem_ld_16x256b(tl + kTmemS + sb * nr + 8 * (g0 + i), s[i]);
         tmem_wait_ld();
         tc_fence_before();
         if (kSBuf == 1) {
@@ -457,20 +456,16 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
         if (mixed) {
 #pragma unroll
           for (int i = 0; i < kG; ++i)
-            if (i < ng) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (t * kTcTile + tok + 8 * (e >> 1) >= low + s_more[8 * (g0 + i) + c0 + (e & 1)])
-                  s[i][e] = 0xff800000u;                 // -inf
-            }
+            for (int e = 0; e < 4; ++e)
+              if (t * kTcTile + tok + 8 * (e >> 1) >= low + s_more[8 * (g0 + i) + c0 + (e & 1)])
+                s[i][e] = 0xff800000u;                   // -inf
         }
 #pragma unroll
         for (int i = 0; i < kG; ++i)
-          if (i < ng) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              top = fmaxf(top, fmaf(__uint_as_float(s[i][e]), c, -m[i][e & 1]));
-          }
+          for (int e = 0; e < 4; ++e)
+            top = fmaxf(top, fmaf(__uint_as_float(s[i][e]), c, -m[i][e & 1]));
         // rows that some query row does not see: nothing that 0 * would turn into a NaN
         if (mixed) {
           const int first = max(low - t * kTcTile, 0), per = sh.rank / 8;
@@ -488,8 +483,7 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
           // a maximum that passed (the first tile's always): weights, sums and O^T go to the
           // maxima of now
 #pragma unroll
-          for (int i = 0; i < kG; ++i)
-            if (i < ng) {
+          for (int i = 0; i < kG; ++i) {
               float a = fmaxf(__uint_as_float(s[i][0]), __uint_as_float(s[i][2]));
               float b = fmaxf(__uint_as_float(s[i][1]), __uint_as_float(s[i][3]));
 #pragma unroll
@@ -511,12 +505,10 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
           if (named_bar_or(1, kSoft, !ok)) { dead = true; break; }
 #pragma unroll
           for (int i = 0; i < kG; ++i)
-            if (i < ng) {
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                l[i][e] *= s_row[8 * (g0 + i) + c0 + e];
-                m[i][e] = s_m[8 * (g0 + i) + c0 + e];
-              }
+            for (int e = 0; e < 2; ++e) {
+              l[i][e] *= s_row[8 * (g0 + i) + c0 + e];
+              m[i][e] = s_m[8 * (g0 + i) + c0 + e];
             }
           if (t > p.t0) {
             tc_fence_after();
@@ -542,7 +534,7 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
           float x[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            x[e] = i < ng ? ex2(fmaf(__uint_as_float(s[i][e]), c, -m[i][e & 1])) : 0.f;
+            x[e] = ex2(fmaf(__uint_as_float(s[i][e]), c, -m[i][e & 1]));
           l[i][0] += x[0] + x[2];
           l[i][1] += x[1] + x[3];
           pk[i][0] = pack_bf16(x[0], x[1]);
@@ -553,13 +545,12 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
         const uint32_t pr = smem_u32(sp + pb * pl.p_bytes);
         const uint32_t at = 16 * wq + (lane & 15);
 #pragma unroll
-        for (int i = 0; i < kG; i += 2) {
-          if (i + 1 < ng)
-            stmatrix_x4(pr + chunk_mnmajor_sw32(g0 + i + (lane >> 4), at, kTcTile), pk[i][0],
-                        pk[i][1], pk[i + 1 < kG ? i + 1 : i][0], pk[i + 1 < kG ? i + 1 : i][1]);
-          else if (i < ng)
-            stmatrix_x2(pr + chunk_mnmajor_sw32(g0 + i, at, kTcTile), pk[i][0], pk[i][1]);
-        }
+        for (int i = 0; i + 1 < kG; i += 2)
+          stmatrix_x4(pr + chunk_mnmajor_sw32(g0 + i + (lane >> 4), at, kTcTile), pk[i][0],
+                      pk[i][1], pk[i + 1][0], pk[i + 1][1]);
+        if (kG & 1)
+          stmatrix_x2(pr + chunk_mnmajor_sw32(g0 + kG - 1, at, kTcTile), pk[kG - 1][0],
+                      pk[kG - 1][1]);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.p_full[pb]);
@@ -573,8 +564,7 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
       const bool first = p.t0 == 0, last = p.t1 == p.tiles;
       const int slot = first && last ? -1 : 2 * (int)blockIdx.x + (first ? 1 : 0);
 #pragma unroll
-      for (int i = 0; i < kG; ++i)
-        if (i < ng) {
+      for (int i = 0; i < kG; ++i) {
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) {
             l[i][0] += __shfl_xor_sync(kAll, l[i][0], o);
@@ -597,27 +587,46 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
             make_int4((int)p.row0, p.rows, latent_cta_of(p.pos + p.tiles - 1, st.W, st.G), 0);
       named_bar(1, kSoft);
       tc_fence_after();
-      for (int j = half; j < npair; j += 2) {
-        const int d = 128 * j + 32 * wq + lane;
-#pragma unroll 1
-        for (int i = 0; i < p.rows; i += 16) {
-          uint32_t o[16];
-          tmem_ld16(tl + j * nr + i, o);
-          tmem_wait_ld();
-          if (slot < 0) {
+      // 16 rows a load, the next one's under the stores: each stores 32 columns of a row a warp
+      const int nc = (p.rows + 15) / 16, n = nc * ((npair - half + 1) / 2);
+      uint32_t o[2][16];
+      auto fetch = [&](int u, uint32_t (&v)[16]) {       // u-th of this warp's loads
+        tmem_ld16(tl + (half + 2 * (u / nc)) * nr + 16 * (u % nc), v);
+      };
+      auto put = [&](int u, const uint32_t (&v)[16]) {
+        const int i = 16 * (u % nc), d = 128 * (half + 2 * (u / nc)) + 32 * wq + lane;
+        const int rows = min(p.rows - i, 16);
+        float f[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              if (i + e < p.rows)
-                out[(p.row0 + i + e) * sh.rank + d] =
-                    __float2bfloat16_rn(__uint_as_float(o[e]) * s_row[i + e]);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              if (i + e < p.rows)
-                pt.o[((long long)slot * nr + i + e) * sh.rank + d] =
-                    __uint_as_float(o[e]) * s_row[i + e];
-          }
+        for (int e = 0; e < 16; e += 4) {
+          const float4 w = *reinterpret_cast<const float4*>(s_row + i + e);
+          f[e] = __uint_as_float(v[e]) * w.x;
+          f[e + 1] = __uint_as_float(v[e + 1]) * w.y;
+          f[e + 2] = __uint_as_float(v[e + 2]) * w.z;
+          f[e + 3] = __uint_as_float(v[e + 3]) * w.w;
         }
+        if (slot < 0) {
+          bf16* y = out + (p.row0 + i) * sh.rank + d;
+#pragma unroll
+          for (int e = 0; e < 16; ++e, y += sh.rank)
+            if (e < rows) *y = __float2bfloat16_rn(f[e]);
+        } else {
+          float* y = pt.o + ((long long)slot * nr + i) * sh.rank + d;
+#pragma unroll
+          for (int e = 0; e < 16; ++e, y += sh.rank)
+            if (e < rows) *y = f[e];
+        }
+      };
+      if (n > 0) fetch(0, o[0]);
+#pragma unroll 1
+      for (int u = 0; u < n; u += 2) {
+        tmem_wait_ld();
+        if (u + 1 < n) fetch(u + 1, o[1]);
+        put(u, o[0]);
+        if (u + 1 >= n) break;
+        tmem_wait_ld();
+        if (u + 2 < n) fetch(u + 2, o[0]);
+        put(u + 1, o[1]);
       }
       tc_fence_before();
       named_bar(1, kSoft);                               // the block's rows are done with
@@ -698,7 +707,7 @@ cudaError_t launch_latent_tc(const void* q, const void* cache, const int32_t* pa
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   note_launches(1);
-  return launch_latent_join(out, lse, pt, G, nr, sh.rank, KDA_BF16, stream);
+  return launch_latent_join(out, lse, pt, G, nr, sh.rank, latent_items(sh, nr), KDA_BF16, stream);
 }
 
 // Reads (and with reset clears) g_latent_timeout; host side of kda_device_status.
