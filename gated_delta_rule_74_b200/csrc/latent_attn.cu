@@ -14,6 +14,8 @@
 // partial sums meet in shared memory.  Output: a thread holds eight rows by rank / 128
 // columns in registers (three reads for 8 rank / 128 FMAs).  Bound by the FMAs and these
 // reads, not by the cache's bytes: fp32 has no tensor-core form of fp32 accuracy.
+#include <type_traits>
+
 #include "latent_attn.cuh"
 #include "sm100.cuh"
 
@@ -78,37 +80,34 @@ kda_latent_simt_kernel(const T* __restrict__ q, const T* __restrict__ cache,
   if (tid == 0) pt.head[blockIdx.x] = make_int4(0, 0, 0, 0);
 
   constexpr int E = 16 / sizeof(T);
-  const int DE = D / E;                                     // 16-byte pieces of a row
   const int r = tid >> 4, j0 = tid & 15;                    // softmax: row r, tokens j0, j0 + 16
   const int rg = lane >> 3, tg = lane & 7, D8 = D / 8;      // scores: rows rg + 4 a, tokens tg + 8 b
   const int hr = 8 * (tid & 1), d0 = (tid >> 1) * kD;       // output: rows hr .., columns d0 ..
   LatentWalk walk(st);
   LatentPiece p;
   while (walk.next(sh, seq_lens, cu_seqlens, kRows, kTile, &p)) {
-    // tile t into buffer b; zeros where there is no row
+    // tile t into buffer b, eight threads a row; zeros where there is no row
     auto fetch = [&](int t, int b) {
-      for (int i = tid; i < kTile * DE; i += kNT) {
-        const int row = i / DE, e = (i - row * DE) * E;
-        const int pos = t * kTile + row;
-        const T* src = cache;
-        uint32_t bytes = 0;
-        if (pos < p.len) {
-          const int pg = pos / sh.page_size;
-          const int page = __ldg(page_table + (long long)p.n * sh.max_pages + pg);
-          if (page >= 0 && page < sh.num_pages) {
-            src = cache + page * sh.page_stride + (pos - pg * sh.page_size) * sh.row_stride + e;
-            bytes = 16;
-          }
+      const int row = tid >> 3, pos = t * kTile + row;
+      const T* src = cache;
+      uint32_t bytes = 0;
+      if (pos < p.len) {
+        const int pg = pos / sh.page_size;
+        const int page = __ldg(page_table + (long long)p.n * sh.max_pages + pg);
+        if (page >= 0 && page < sh.num_pages) {
+          src = cache + page * sh.page_stride + (pos - pg * sh.page_size) * sh.row_stride;
+          bytes = 16;
         }
-        cp_async16(sk + (b * kTile + row) * LD + e, src, bytes);
       }
+      for (int e = (tid & 7) * E; e < D; e += 8 * E)
+        cp_async16(sk + (b * kTile + row) * LD + e, src + (bytes ? e : 0), bytes);
       cp_async_commit();
     };
     __syncthreads();                                        // the block before is done with
-    for (int i = tid; i < kRows * DE; i += kNT) {
-      const int row = i / DE, e = (i - row * DE) * E;
-      cp_async16(sq + row * LD + e, q + (p.row0 + (row < p.rows ? row : 0)) * D + e,
-                 row < p.rows ? 16 : 0);
+    {
+      const int row = tid >> 4, from = row < p.rows ? row : 0;
+      for (int e = (tid & 15) * E; e < D; e += 16 * E)
+        cp_async16(sq + row * LD + e, q + (p.row0 + from) * D + e, row < p.rows ? 16 : 0);
     }
     fetch(p.t0, 0);
     float acc[8][kD];
@@ -184,18 +183,23 @@ kda_latent_simt_kernel(const T* __restrict__ q, const T* __restrict__ cache,
 #pragma unroll
         for (int k = 0; k < kD; ++k) acc[i][k] *= s_alpha[hr + i];
       const T* v0 = sk + b * kTile * LD + d0;
+      auto add_values = [&](auto all) {                     // all: every row sees every token
 #pragma unroll 4
-      for (int j = 0; j < kTile; ++j) {
-        float v[kD], w[8];
-        load_few<kD>(v0 + j * LD, v);
-        *reinterpret_cast<float4*>(w) = *reinterpret_cast<const float4*>(&sp[j][hr]);
-        *reinterpret_cast<float4*>(w + 4) = *reinterpret_cast<const float4*>(&sp[j][hr + 4]);
+        for (int j = 0; j < kTile; ++j) {
+          float v[kD], w[8];
+          load_few<kD>(v0 + j * LD, v);
+          *reinterpret_cast<float4*>(w) = *reinterpret_cast<const float4*>(&sp[j][hr]);
+          *reinterpret_cast<float4*>(w + 4) = *reinterpret_cast<const float4*>(&sp[j][hr + 4]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+          for (int i = 0; i < 8; ++i)
 #pragma unroll
-          for (int k = 0; k < kD; ++k)                      // a weight of zero takes nothing, not 0 * inf
-            acc[i][k] = mixed && w[i] == 0.f ? acc[i][k] : fmaf(w[i], v[k], acc[i][k]);
-      }
+            for (int k = 0; k < kD; ++k)                    // a weight of zero takes nothing, not 0 * inf
+              acc[i][k] = !decltype(all)::value && w[i] == 0.f ? acc[i][k]
+                                                               : fmaf(w[i], v[k], acc[i][k]);
+        }
+      };
+      if (mixed) add_values(std::false_type());
+      else add_values(std::true_type());
       __syncthreads();                                      // the tile and its weights are used
     }
     // ---- results: whole blocks to the output, shared ones to a partial slot
