@@ -18,18 +18,18 @@
 // memory and tensor cores at 96 rows.
 //
 // One CTA an SM, its stretch of tiles as latent_attn.cuh lays it out.  Warps 0 and 2 bring
-// the tiles by TMA into a ring of stages (256 columns x 64 rows; the rope columns apart), one
-// box a run of rows inside of a page, warp 3 Q; warp 1 issues the MMAs; warps 4..11 do the
-// softmax (two warps a lane quarter of 16 tokens, half of the rows each; a thread holds two
-// tokens and two of every eight rows), the rare rescaling of O^T and the results (thread =
-// value column).  The maximum that the weights refer to moves only when a score passes it
-// by 2^8: a tile then needs one vote, no reduction over the tokens, O^T is rescaled a few
-// times a sequence, and the weights stay below 2^8, far inside of bf16 and fp32.  Sums are
-// kept by thread and joined at the end of a block.
-// The scores of tile t + 1 are issued while tile t's softmax runs, as far as stages allow
-// (all of them up to 64 rows, half of the columns at 96); whichever of "the next stage is
-// there" and "the weights are there" comes first goes first.  A wait between MMAs costs
-// their warp 300 to 450 cycles, as long as eight of the MMAs take, so stages are large.
+// the tiles by TMA into a ring, eight tokens with all their columns a box (so that pages of any
+// multiple of eight do), warp 3 Q; warp 1 issues the MMAs; warps 4..11 do the softmax (two
+// warps a lane quarter of 16 tokens, half of the rows each; a thread holds two tokens and two
+// of every eight rows), the rare rescaling of O^T and the results (thread = value column).
+// The maximum that the weights refer to moves only when a score passes it by 2^8: a tile then
+// needs one vote, no reduction over the tokens, O^T is rescaled a few times a sequence, and
+// the weights stay below 2^8, far inside of bf16 and fp32.  Sums are kept by thread and
+// joined at the end of a block.
+// The scores of tile t + 1 go before the values of tile t when the tile is there before the
+// weights are.  The values' products run over 16 tokens at a time and hand those back to the
+// producers at once.  A wait between MMAs costs their warp 300 to 450 cycles, as long as eight
+// of the MMAs take: a tile costs two.
 //
 // Rows of the tile that some query row does not see (the causal edge, what lies behind the
 // length in the last page) have weights of exactly zero; their infinities and NaN would
@@ -50,55 +50,54 @@ using bf16 = __nv_bfloat16;
 
 constexpr int kTcThreads = 384;
 constexpr int kSoft = 256;                         // threads of warps 4..11
-constexpr int kTcTile = 64;
 constexpr int kTcMaxRows = 96;
-constexpr uint32_t kChunk = 64 * 128;              // 64 cached rows x 64 columns
-constexpr uint32_t kPair = 2 * kChunk;
-constexpr int kMaxStages = 8;
-constexpr uint32_t kTcSmem = 229376;               // Q, stages, P
+constexpr int kMaxTiles = 4;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kWaitLimit = 1u << 22, kPollLimit = 1u << 26, kDrainLimit = 1u << 14;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kNone = -1e30f;                    // maximum of a row that has seen nothing
 
-// How shared memory is divided, from the block's rows and the row's columns.
+// Tokens of a tile.  64 fill the MMAs' M side; 48 where only one tile of 64 would fit beside Q
+// (148 sequences of 8192 tokens and 96 heads: 401 us against 419 with one and a half).  At 48
+// rows three tiles of 48 would fit, but two of 64 are faster (85 us against 92 for four
+// drafts of 64 sequences), and so at 16 rows (219 against 234 us for 256 sequences).
+__host__ __device__ constexpr int tc_tile(int nr) { return nr >= 80 ? 48 : 64; }
+// Dynamic shared memory: all but 3 KB of the 227 (2 KB at 96 rows) for the variables.
+__host__ __device__ constexpr uint32_t tc_smem(int nr) { return nr > 80 ? 230400 : 229376; }
+
+// How shared memory is divided, from the block's rows and the row's columns: a ring of tiles,
+// Q, P.  A tile is groups of eight tokens, a group all of a row's 64-column chunks one after
+// the other, a chunk [8][128 B] with the 128-byte swizzle; a group comes by one TMA box.
 struct TcPlan {
   int nr;                           // rows of a block, a multiple of 16 up to 96
-  int npair;                        // rank / 128
-  int spair, ns;                    // pairs of a stage, stages of a tile
-  int nq, np;                       // Q and P buffers
-  int stages, rope_slots;
-  uint32_t q_bytes, p_bytes;
-  int box_rows, groups;             // rows of a TMA box; boxes for 64 rows of one chunk
+  int npair, nch;                   // rank / 128; chunks of a row
+  int ntile, nq, np;                // tiles of the ring; Q and P buffers
+  uint32_t group, tile_bytes, q_bytes, p_bytes;
 };
 
 // Q is buffered twice while it is small (a decode step changes blocks every few tiles), P
-// and the rope columns while the stages then still hold two tiles.
-TcPlan tc_plan(int nr, int rank, int rope, int page_size) {
+// where there is room beside the tiles.
+TcPlan tc_plan(int nr, int rank, int rope) {
   TcPlan p;
+  const int kt = tc_tile(nr);
   p.nr = nr;
   p.npair = rank / 128;
-  p.spair = p.npair < 2 ? 1 : 2;
-  p.ns = (p.npair + 1) / 2;
-  p.q_bytes = (uint32_t)nr * (rank + rope) * 2;
-  p.p_bytes = (uint32_t)nr * 128;
+  p.nch = (rank + rope) / 64;
+  p.group = (uint32_t)p.nch * 1024;
+  p.tile_bytes = kt / 8 * p.group;
+  p.q_bytes = (uint32_t)nr * p.nch * 128;
+  p.p_bytes = (uint32_t)nr * kt * 2;
   p.nq = nr <= 32 ? 2 : 1;
-  p.np = nr <= 64 ? 2 : 1;
-  const uint32_t left = kTcSmem - p.nq * p.q_bytes - p.np * p.p_bytes, stage = p.spair * kPair;
-  p.rope_slots = rope ? 2 : 0;
-  if (rope && (int)((left - 2 * kChunk) / stage) < 2 * p.ns) p.rope_slots = 1;
-  p.stages = (int)((left - p.rope_slots * kChunk) / stage);
-  if (p.stages > kMaxStages) p.stages = kMaxStages;
-  p.box_rows = kTcTile;
-  while (page_size % p.box_rows) p.box_rows /= 2;
-  p.groups = kTcTile / p.box_rows;
+  const uint32_t fixed = p.nq * p.q_bytes + p.p_bytes;
+  p.ntile = (int)((tc_smem(nr) - fixed) / p.tile_bytes);
+  if (p.ntile > kMaxTiles) p.ntile = kMaxTiles;
+  p.np = fixed + p.ntile * p.tile_bytes + p.p_bytes <= tc_smem(nr) ? 2 : 1;
   return p;
 }
 
 struct TcBars {
   uint64_t q_full[2], q_empty[2];
-  uint64_t full[kMaxStages], empty[kMaxStages][2];      // empty: by pair of the stage
-  uint64_t rope_empty[2];
+  uint64_t full[kMaxTiles], empty[kMaxTiles][4];   // empty: by 16 tokens of the tile
   uint64_t s_full[2], s_empty;
   uint64_t p_full[2], pv_done[2];
   uint64_t o_empty, drain;
@@ -120,31 +119,28 @@ template <int NR>
 __global__ void __launch_bounds__(kTcThreads, 1)
 kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                      const __grid_constant__ CUtensorMap c_map,
-                     const __grid_constant__ CUtensorMap r_map,
                      const int32_t* __restrict__ page_table,
                      const int32_t* __restrict__ seq_lens,
                      const int32_t* __restrict__ cu_seqlens, bf16* __restrict__ out,
                      float* __restrict__ lse, LatentAttnShape sh, TcPlan pl, LatentPartials pt) {
-  // the alignment is part of the declaration: there is no room to round up (a block of 96 rows
-  // fills the 227 KB, 3 KB of them the variables below)
+  constexpr int nr = NR, KT = tc_tile(NR), KK = KT / 16, kSBuf = NR <= 80 ? 2 : 1;
+  constexpr uint32_t kTmemS = 4 * NR;
+  // the alignment is part of the declaration: there is no room to round up
   extern __shared__ __align__(1024) uint8_t sm[];
   __shared__ TcBars bar;
   __shared__ LatentStart st;
-  __shared__ long long s_sum[33];
   __shared__ float s_m[NR];                         // maxima the weights refer to, scaled
   __shared__ uint8_t s_more[NR];                    // tokens each row sees more than the first
   __shared__ __align__(16) float s_row[NR];         // rescaling factors, then 1 / sum
-  __shared__ float s_red[4][NR];                    // the lane quarters' maxima, then sums
+  // two lane quarters' maxima or sums at a time; before, the sums of latent_find_start
+  __shared__ __align__(16) float s_red[2 * NR < 68 ? 68 : 2 * NR];
   __shared__ uint32_t s_tmem;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int nr = NR, kSBuf = NR <= 80 ? 2 : 1;
-  constexpr uint32_t kTmemS = 4 * NR;
   const int npair = pl.npair;
-  const uint32_t stage_bytes = pl.spair * kPair;
-  uint8_t* const sq = sm;
-  uint8_t* const sst = sq + pl.nq * pl.q_bytes;
-  uint8_t* const srope = sst + pl.stages * stage_bytes;
-  uint8_t* const sp = srope + pl.rope_slots * kChunk;
+  // the ring first: the MMAs' 64 rows of a 48-token tile reach 16 rows behind it, into Q
+  uint8_t* const ring = sm;
+  uint8_t* const sq = ring + pl.ntile * pl.tile_bytes;
+  uint8_t* const sp = sq + pl.nq * pl.q_bytes;
 
   if (warp == 1) {
     tmem_alloc(&s_tmem, kTmemCols);
@@ -154,15 +150,13 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.q_full[i], 1);
       mbar_init(&bar.q_empty[i], 1);
-      mbar_init(&bar.rope_empty[i], 1);
       mbar_init(&bar.s_full[i], 1);
       mbar_init(&bar.p_full[i], kSoft / 32);
       mbar_init(&bar.pv_done[i], 1);
     }
-    for (int i = 0; i < kMaxStages; ++i) {
-      mbar_init(&bar.full[i], 2);                   // warps 0 and 2
-      mbar_init(&bar.empty[i][0], 1);
-      mbar_init(&bar.empty[i][1], 1);
+    for (int i = 0; i < kMaxTiles; ++i) {
+      mbar_init(&bar.full[i], KK);
+      for (int k = 0; k < 4; ++k) mbar_init(&bar.empty[i][k], 1);
     }
     mbar_init(&bar.s_empty, kSoft / 32);
     mbar_init(&bar.o_empty, kSoft / 32);
@@ -170,79 +164,59 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
     fence_mbar_init();
     pt.head[blockIdx.x] = make_int4(0, 0, 0, 0);
   }
-  latent_find_start(sh, seq_lens, cu_seqlens, nr, kTcTile, &st, s_sum);
+  latent_find_start(sh, seq_lens, cu_seqlens, nr, KT, &st, reinterpret_cast<long long*>(s_red));
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tb = s_tmem;
   grid_dep_launch();                                // the join may be made ready
-  const bool rope = sh.rope != 0;
   bool ok = true;
   constexpr uint32_t kAll = 0xffffffffu;
 
   if (warp == 0 || warp == 2) {
     // ------------------------------------------------------------- tiles by TMA
-    // Warp 0 brings the first pair of each stage, warp 2 the second and the rope columns.
-    const int w = warp >> 1;
+    // 16 tokens (two groups) at a time, the two warps in turn: one warp's loop (wait, look up,
+    // arm, copy; 400 to 600 cycles) alone holds the stream below 4 TB/s.
     LatentWalk walk(st);
     LatentPiece p;
-    uint32_t stage = 0, use = 0, rs = 0, ruse = 0;
-    const uint32_t step = pl.box_rows * 128;
-    while (ok && walk.next(sh, seq_lens, cu_seqlens, nr, kTcTile, &p)) {
-      // lane's box of tile t: rows [64 t + lane box_rows, ..) of the sequence; a page past the
-      // cache (zeros) where there is none
+    uint32_t slot = 0, use = 0, turn = 0;
+    while (ok && walk.next(sh, seq_lens, cu_seqlens, nr, KT, &p)) {
+      // lane's group of tile t: its page (one past the cache, which reads as zeros, where there
+      // is none)
       auto look = [&](int t) {
-        const int pos = t * kTcTile + lane * pl.box_rows;
-        if (lane >= pl.groups || t >= p.t1 || pos >= p.len) return sh.num_pages;
+        const int pos = t * KT + 8 * lane;
+        if (lane >= KT / 8 || t >= p.t1 || pos >= p.len) return sh.num_pages;
         const int id = __ldg(page_table + (long long)p.n * sh.max_pages + pos / sh.page_size);
         return id >= 0 && id < sh.num_pages ? id : sh.num_pages;
       };
       int next_page = look(p.t0);
       for (int t = p.t0; t < p.t1 && ok; ++t) {
-        const int page = next_page, row = (t * kTcTile + lane * pl.box_rows) % sh.page_size;
+        const int page = next_page, row = (t * KT + 8 * lane) % sh.page_size;
         next_page = look(t + 1);
-        for (int s = 0; s < pl.ns; ++s) {
-          if (use > 0) ok = __all_sync(kAll, mbar_wait(&bar.empty[stage][w], (use - 1) & 1, kWaitLimit));
-          const bool with_rope = rope && w == 1 && s == 0;
-          if (with_rope && ruse > 0)
-            ok = ok && __all_sync(kAll, mbar_wait(&bar.rope_empty[rs], (ruse - 1) & 1, kWaitLimit));
+        uint8_t* const d = ring + slot * pl.tile_bytes;
+        for (int k = 0; k < KK; ++k, turn ^= 1) {
+          if (turn != (uint32_t)(warp >> 1)) continue;
+          if (use > 0) ok = __all_sync(kAll, mbar_wait(&bar.empty[slot][k], (use - 1) & 1, kWaitLimit));
           if (!ok) break;
-          const int pair = s * pl.spair + w;
-          const bool some = w < pl.spair && pair < npair;
-          uint8_t* const d = sst + stage * stage_bytes + w * kPair;
-          uint8_t* const dr = srope + rs * kChunk;
-          uint64_t* const full = &bar.full[stage];
-          if (elect_one())
-            mbar_arrive_expect_tx(full, (some ? kPair : 0u) + (with_rope ? kChunk : 0u));
+          const int pg0 = __shfl_sync(kAll, page, 2 * k), rw0 = __shfl_sync(kAll, row, 2 * k);
+          const int pg1 = __shfl_sync(kAll, page, 2 * k + 1), rw1 = __shfl_sync(kAll, row, 2 * k + 1);
+          if (elect_one()) {
+            mbar_arrive_expect_tx(&bar.full[slot], 2 * pl.group);
+            tma_load_4d(d + 2 * k * pl.group, &c_map, 0, rw0, 0, pg0, &bar.full[slot]);
+            tma_load_4d(d + (2 * k + 1) * pl.group, &c_map, 0, rw1, 0, pg1, &bar.full[slot]);
+          }
           __syncwarp();
-          for (int b = 0; b < pl.groups; ++b) {
-            const int pg = __shfl_sync(kAll, page, b), rw = __shfl_sync(kAll, row, b);
-            if (elect_one()) {
-              if (with_rope) tma_load_4d(dr + b * step, &r_map, 0, rw, 2 * npair, pg, full);
-              if (some && pl.groups == 1) {
-                tma_load_4d(d, &c_map, 0, rw, 2 * pair, pg, full);
-              } else if (some) {                         // a chunk's boxes lie 64 rows apart
-                tma_load_4d(d + b * step, &r_map, 0, rw, 2 * pair, pg, full);
-                tma_load_4d(d + b * step + kChunk, &r_map, 0, rw, 2 * pair + 1, pg, full);
-              }
-            }
-            __syncwarp();
-          }
-          if (with_rope && ++rs == (uint32_t)pl.rope_slots) {
-            rs = 0;
-            ++ruse;
-          }
-          if (++stage == (uint32_t)pl.stages) {
-            stage = 0;
-            ++use;
-          }
+        }
+        if (++slot == (uint32_t)pl.ntile) {
+          slot = 0;
+          ++use;
         }
       }
     }
     // let copies in flight land before the memory goes away (those that never started cost
     // the limit)
-    for (uint32_t i = 0; !ok && i < (uint32_t)pl.stages; ++i) {
-      const uint32_t uses = use + (i < stage ? 1 : 0);
+    for (uint32_t i = 0; !ok && i < (uint32_t)pl.ntile; ++i) {
+      const uint32_t uses = use + (i <= slot ? 1 : 0);
       if (uses) mbar_wait(&bar.full[i], (uses - 1) & 1, kDrainLimit);
     }
   } else if (warp == 3) {
@@ -250,7 +224,7 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
     LatentWalk walk(st);
     LatentPiece p;
     uint32_t qi = 0, quse = 0;
-    while (ok && walk.next(sh, seq_lens, cu_seqlens, nr, kTcTile, &p)) {
+    while (ok && walk.next(sh, seq_lens, cu_seqlens, nr, KT, &p)) {
       if (quse > 0) ok = __all_sync(kAll, mbar_wait(&bar.q_empty[qi], (quse - 1) & 1, kWaitLimit));
       if (!ok) break;
       if (elect_one()) {
@@ -270,128 +244,102 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
   } else if (warp == 1) {
     // ------------------------------------------------------------- the MMAs
     // The whole warp runs the loop, one lane issues (see elect_one).
-    const uint32_t id_qk = idesc_bf16(kTcTile, nr, false, false);
+    const uint32_t id_qk = idesc_bf16(64, nr, false, false);
     const uint32_t id_pv = idesc_bf16(128, nr, true, true);
-    // first descriptors; a K step is 32 bytes further in a K-major block, 2048 in V, 512 in P
+    // first descriptors.  The tile's groups of eight tokens lie `group` bytes apart, as the
+    // rows of the scores' operand and as the K index of the values'; a K step of the scores
+    // is 32 bytes further in a chunk, of the values two groups, of P 512 bytes
     const uint64_t dq = desc_kmajor_sw128(smem_u32(sq), nr, 0);
-    const uint64_t dk = desc_kmajor_sw128(smem_u32(sst), kTcTile, 0);
-    const uint64_t dr = desc_kmajor_sw128(smem_u32(srope), kTcTile, 0);
-    const uint64_t dv = desc_mnmajor_sw128(smem_u32(sst), kTcTile, 0);
-    const uint64_t dp = desc_mnmajor_sw32(smem_u32(sp), kTcTile, 0);
-    const uint32_t block = (uint32_t)(nr * 8);            // 64 columns of Q, in 16 bytes
-    const int early = min(pl.ns, pl.stages - pl.ns);      // stages of scores ahead of the values
+    const uint64_t dk = smem_desc(smem_u32(ring), 16, pl.group, kSw128);
+    const uint64_t dv = smem_desc(smem_u32(ring), 1024, pl.group, kSw128);
+    const uint64_t dp = desc_mnmajor_sw32(smem_u32(sp), KT, 0);
     LatentWalk walk(st);
     LatentPiece p;
     uint32_t it = 0, g = 0;                              // blocks, tiles
-    uint32_t rs = 0, stage = 0, use = 0;                 // of the next scores
-    uint32_t vstage = 0;                                 // of the next values
+    uint32_t slot = 0, use = 0, vslot = 0;               // of the next scores and values
     uint32_t qi = 0, quse = 0;
-    // stage s of the scores of tile `t` (it is there)
-    auto issue_qk = [&](int s, uint32_t t, uint64_t q0) {
+    // the scores of tile `t` (it is there)
+    auto issue_qk = [&](uint32_t t, uint64_t q0) {
       const uint32_t d = tb + kTmemS + (kSBuf == 2 ? t & 1 : 0) * nr;
-      const uint64_t a = q0 + (uint64_t)(2 * s * pl.spair * block);
-      const uint64_t b = dk + (uint64_t)(stage * (stage_bytes / 16));
-      const uint64_t ra = q0 + (uint64_t)(2 * npair * block), rb = dr + (uint64_t)(rs * (kChunk / 16));
-      const bool two = s * pl.spair + 1 < npair && pl.spair == 2;
+      const uint64_t k0 = dk + (uint64_t)(slot * (pl.tile_bytes / 16));
       if (elect_one()) {
-        if (rope && s == 0) {
+        for (int c = 0; c < pl.nch; ++c) {
+          const uint64_t a = k0 + (uint64_t)(c * 64), b = q0 + (uint64_t)(c * nr * 8);
+          mma_ss_all(d, a, b, id_qk, c > 0);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) mma_ss_all(d, rb + 2 * kk, ra + 2 * kk, id_qk, kk > 0);
-          mma_commit(&bar.rope_empty[rs]);
+          for (int i = 1; i < 4; ++i) mma_ss_all(d, a + 2 * i, b + 2 * i, id_qk, 1);
         }
-        mma_ss_all(d, b, a, id_qk, rope || s > 0);
-#pragma unroll
-        for (int kk = 1; kk < 8; ++kk)
-          mma_ss_all(d, b + (kk >> 2) * (kChunk / 16) + 2 * (kk & 3), a + (kk >> 2) * block + 2 * (kk & 3),
-                     id_qk, 1);
-        if (two) {
-#pragma unroll
-          for (int kk = 8; kk < 16; ++kk)
-            mma_ss_all(d, b + (kk >> 2) * (kChunk / 16) + 2 * (kk & 3),
-                       a + (kk >> 2) * block + 2 * (kk & 3), id_qk, 1);
-        }
-        if (s == pl.ns - 1) mma_commit(&bar.s_full[kSBuf == 2 ? t & 1 : 0]);
+        mma_commit(&bar.s_full[kSBuf == 2 ? t & 1 : 0]);
       }
       __syncwarp();
-      if (rope && s == 0 && ++rs == (uint32_t)pl.rope_slots) rs = 0;
-      if (++stage == (uint32_t)pl.stages) {
-        stage = 0;
+      if (++slot == (uint32_t)pl.ntile) {
+        slot = 0;
         ++use;
       }
     };
-
-    auto s_free = [&](uint32_t t) {                      // one buffer: tile t - 1 has been read
-      const bool f = t == 0 || __all_sync(kAll, mbar_test_wait(&bar.s_empty, (t - 1) & 1));
+    // one score buffer: whether tile t - 1 has been read from it
+    auto s_free = [&](uint32_t t) {
+      if (kSBuf == 2 || t == 0) return true;
+      const bool f = __all_sync(kAll, mbar_test_wait(&bar.s_empty, (t - 1) & 1));
       if (f) tc_fence_after();
       return f;
     };
 
-    while (ok && walk.next(sh, seq_lens, cu_seqlens, nr, kTcTile, &p)) {
+    while (ok && walk.next(sh, seq_lens, cu_seqlens, nr, KT, &p)) {
       const uint64_t q0 = dq + (uint64_t)(qi * (pl.q_bytes / 16));
       const int nt = p.t1 - p.t0;
       ok = __all_sync(kAll, mbar_wait(&bar.q_full[qi], quse & 1, kWaitLimit));
-      int s = 0;                                         // next stage of the scores of tile i
       for (int i = 0; i <= nt && ok; ++i) {
-        // scores of tile i (g + 1 for i > 0) and, between them, the values of tile i - 1.  With two
-        // score buffers their place was read by the softmax of the tile before last, whose
-        // weights have been used; with one, by the last tile's (s_empty).
+        // scores of tile i (g + 1 for i > 0) and, before or after them, the values of tile i - 1,
+        // whichever can go first.  With two score buffers the place was read by the softmax of
+        // the tile before last, whose weights have been used; with one, by the last tile's.
         const uint32_t ts = i == 0 ? g : g + 1;
-        const bool scores = i < nt;
+        bool scores = i < nt;
         if (i > 0) {
           const uint32_t pb = pl.np == 2 ? g & 1 : 0, ppar = (pl.np == 2 ? g >> 1 : g) & 1;
-          uint32_t polls = 0;
-          while (ok && (!scores || s >= early)) {        // nothing else can be done before
-            ok = __all_sync(kAll, mbar_wait(&bar.p_full[pb], ppar, kWaitLimit));
-            break;
-          }
-          while (ok && !__all_sync(kAll, mbar_test_wait(&bar.p_full[pb], ppar))) {
-            if (scores && s < early && (kSBuf == 2 || s > 0 || s_free(ts)) &&
-                __all_sync(kAll, mbar_test_wait(&bar.full[stage], use & 1)))
-              issue_qk(s++, ts, q0);
-            if (++polls > kPollLimit) ok = false;
+          for (uint32_t polls = 0; ok; ++polls) {
+            if (!scores) {                               // nothing else can be done before
+              ok = __all_sync(kAll, mbar_wait(&bar.p_full[pb], ppar, kWaitLimit));
+              break;
+            }
+            if (__all_sync(kAll, mbar_test_wait(&bar.p_full[pb], ppar))) break;
+            if (s_free(ts) && __all_sync(kAll, mbar_test_wait(&bar.full[slot], use & 1))) {
+              issue_qk(ts, q0);
+              scores = false;
+            }
+            if (polls > kPollLimit) ok = false;
           }
           if (ok && i == 1 && it > 0)                    // the block before has left O^T
             ok = __all_sync(kAll, mbar_wait(&bar.o_empty, (it - 1) & 1, kWaitLimit));
           if (!ok) break;
           tc_fence_after();
-          const uint64_t b = dp + (uint64_t)(pb * (pl.p_bytes / 16));
-          for (int v = 0; v < pl.ns; ++v) {
-            const uint64_t a = dv + (uint64_t)(vstage * (stage_bytes / 16));
-            const uint32_t d = tb + v * pl.spair * nr;
-            const bool two = v * pl.spair + 1 < npair && pl.spair == 2;
-            if (elect_one()) {
-              mma_ss_all(d, a, b, id_pv, i > 1);
+          const uint64_t a0 = dv + (uint64_t)(vslot * (pl.tile_bytes / 16));
+          const uint64_t b0 = dp + (uint64_t)(pb * (pl.p_bytes / 16));
+          if (elect_one()) {
 #pragma unroll
-              for (int kk = 1; kk < 4; ++kk) mma_ss_all(d, a + 128 * kk, b + 32 * kk, id_pv, 1);
-              mma_commit(&bar.empty[vstage][0]);
-              if (two) {
-                mma_ss_all(d + nr, a + kPair / 16, b, id_pv, i > 1);
-#pragma unroll
-                for (int kk = 1; kk < 4; ++kk)
-                  mma_ss_all(d + nr, a + kPair / 16 + 128 * kk, b + 32 * kk, id_pv, 1);
-              }
-              mma_commit(&bar.empty[vstage][1]);
-              if (v == pl.ns - 1) mma_commit(&bar.pv_done[pb]);
+            for (int k = 0; k < KK; ++k) {
+              const uint64_t a = a0 + (uint64_t)(2 * k * (pl.group / 16));
+              for (int j = 0; j < npair; ++j)
+                mma_ss_all(tb + j * nr, a + (uint64_t)(j * 128), b0 + 32 * k, id_pv, k > 0 || i > 1);
+              mma_commit(&bar.empty[vslot][k]);
             }
-            __syncwarp();
-            if (++vstage == (uint32_t)pl.stages) vstage = 0;
+            mma_commit(&bar.pv_done[pb]);
           }
+          __syncwarp();
+          if (++vslot == (uint32_t)pl.ntile) vslot = 0;
           ++g;
         }
         if (scores) {
-          if (kSBuf == 1 && s == 0 && ts > 0) {
+          if (kSBuf == 1 && ts > 0) {
             ok = __all_sync(kAll, mbar_wait(&bar.s_empty, (ts - 1) & 1, kWaitLimit));
             tc_fence_after();
           }
-          while (ok && s < pl.ns) {
-            ok = __all_sync(kAll, mbar_wait(&bar.full[stage], use & 1, kWaitLimit));
-            if (ok) issue_qk(s++, ts, q0);
-          }
-          s = 0;
-          if (i == nt - 1) {
-            if (elect_one()) mma_commit(&bar.q_empty[qi]);
-            __syncwarp();
-          }
+          ok = ok && __all_sync(kAll, mbar_wait(&bar.full[slot], use & 1, kWaitLimit));
+          if (ok) issue_qk(ts, q0);
+        }
+        if (i == nt - 1 && ok) {
+          if (elect_one()) mma_commit(&bar.q_empty[qi]);
+          __syncwarp();
         }
       }
       ++it;
@@ -411,6 +359,7 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
     const int wq = warp & 3, half = (warp - 4) >> 2, ts = tid - 128;
     const int g0 = half * kG;
     const int tok = 16 * wq + (lane >> 2), c0 = 2 * (lane & 3);   // tokens tok, tok + 8
+    const bool act = 16 * wq < KT;                       // the quarter has tokens
     const uint32_t tl = tb + ((uint32_t)(32 * wq) << 16);
     const float c = sh.scale * kLog2e;
     LatentWalk walk(st);
@@ -422,7 +371,7 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
       const uint32_t t = g - back;
       return mbar_wait(&bar.pv_done[pl.np == 2 ? t & 1 : 0], (pl.np == 2 ? t >> 1 : t) & 1, kWaitLimit);
     };
-    while (!dead && walk.next(sh, seq_lens, cu_seqlens, nr, kTcTile, &p)) {
+    while (!dead && walk.next(sh, seq_lens, cu_seqlens, nr, KT, &p)) {
       const int low = p.start + p.row_in_seq / sh.H + 1; // the first row's limit, the least
       if (ts < nr) {                                     // rows behind the block: no weight at all
         s_m[ts] = ts < p.rows ? kNone : INFINITY;
@@ -440,12 +389,13 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
         const uint32_t sb = kSBuf == 2 ? g & 1 : 0;
         ok = ok && mbar_wait(&bar.s_full[sb], (kSBuf == 2 ? g >> 1 : g) & 1, kWaitLimit);
         tc_fence_after();
-        const bool mixed = (t + 1) * kTcTile > low;
+        const bool mixed = (t + 1) * KT > low;
         uint32_t s[kG][4];
+        if (act) {
 #pragma unroll
-        for (int i = 0; i < kG; ++i)
-          tmem_ld_16x256b(tl + kTmemS + sb * nr + 8 * (g0 + i), s[i]);
-        tmem_wait_ld();
+          for (int i = 0; i < kG; ++i) tmem_ld_16x256b(tl + kTmemS + sb * nr + 8 * (g0 + i), s[i]);
+          tmem_wait_ld();
+        }
         tc_fence_before();
         if (kSBuf == 1) {
           __syncwarp();
@@ -453,27 +403,29 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
         }
         // whether some scaled score passes its row's maximum by 2^8
         float top = -INFINITY;
-        if (mixed) {
+        if (act && mixed) {
 #pragma unroll
           for (int i = 0; i < kG; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              if (t * kTcTile + tok + 8 * (e >> 1) >= low + s_more[8 * (g0 + i) + c0 + (e & 1)])
+              if (t * KT + tok + 8 * (e >> 1) >= low + s_more[8 * (g0 + i) + c0 + (e & 1)])
                 s[i][e] = 0xff800000u;                   // -inf
         }
+        if (act) {
 #pragma unroll
-        for (int i = 0; i < kG; ++i)
+          for (int i = 0; i < kG; ++i)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            top = fmaxf(top, fmaf(__uint_as_float(s[i][e]), c, -m[i][e & 1]));
+            for (int e = 0; e < 4; ++e)
+              top = fmaxf(top, fmaf(__uint_as_float(s[i][e]), c, -m[i][e & 1]));
+        }
         // rows that some query row does not see: nothing that 0 * would turn into a NaN
         if (mixed) {
-          const int first = max(low - t * kTcTile, 0), per = sh.rank / 8;
-          for (int i = ts; i < (kTcTile - first) * per; i += kSoft) {
-            const int k = first + i / per, c8 = i % per, pair = c8 >> 4;
-            const uint32_t sg = (g * pl.ns + pair / pl.spair) % pl.stages;
-            uint4* w = reinterpret_cast<uint4*>(sst + sg * stage_bytes + (pair % pl.spair) * kPair +
-                                                ((c8 >> 3) & 1) * kChunk + k * 128 + (c8 & 7) * 16);
+          const int first = max(low - t * KT, 0), per = sh.rank / 8;
+          uint8_t* const tile = ring + g % pl.ntile * pl.tile_bytes;
+          for (int i = ts; i < (KT - first) * per; i += kSoft) {
+            const int k = first + i / per, c8 = i % per;
+            uint4* w = reinterpret_cast<uint4*>(tile + (k >> 3) * pl.group + (c8 >> 3) * 1024 +
+                                                (k & 7) * 128 + (c8 & 7) * 16);
             const uint4 a = *w;
             const uint4 b = make_uint4(zero_bad(a.x), zero_bad(a.y), zero_bad(a.z), zero_bad(a.w));
             if (a.x != b.x || a.y != b.y || a.z != b.z || a.w != b.w) *w = b;
@@ -482,8 +434,9 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
         if (named_bar_or(1, kSoft, top > 8.f || !ok)) {
           // a maximum that passed (the first tile's always): weights, sums and O^T go to the
           // maxima of now
+          auto maxima = [&](bool with) {                 // with: those of another quarter
 #pragma unroll
-          for (int i = 0; i < kG; ++i) {
+            for (int i = 0; i < kG; ++i) {
               float a = fmaxf(__uint_as_float(s[i][0]), __uint_as_float(s[i][2]));
               float b = fmaxf(__uint_as_float(s[i][1]), __uint_as_float(s[i][3]));
 #pragma unroll
@@ -491,13 +444,20 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                 a = fmaxf(a, __shfl_xor_sync(kAll, a, o));
                 b = fmaxf(b, __shfl_xor_sync(kAll, b, o));
               }
-              if (lane < 4) *reinterpret_cast<float2*>(&s_red[wq][8 * (g0 + i) + c0]) = make_float2(a, b);
+              float* d = s_red + (wq & 1) * nr + 8 * (g0 + i) + c0;
+              if (lane < 4) {
+                d[0] = with ? fmaxf(a, d[0]) : a;
+                d[1] = with ? fmaxf(b, d[1]) : b;
+              }
             }
+          };
+          if (wq < 2) maxima(false);
+          named_bar(1, kSoft);
+          if (wq >= 2 && act) maxima(true);
           named_bar(1, kSoft);
           if (ts < nr) {
             const float mo = s_m[ts];
-            const float mn = fmaxf(mo, c * fmaxf(fmaxf(s_red[0][ts], s_red[1][ts]),
-                                                 fmaxf(s_red[2][ts], s_red[3][ts])));
+            const float mn = fmaxf(mo, c * fmaxf(s_red[ts], s_red[nr + ts]));
             s_row[ts] = mo == mn ? 1.f : ex2(mo - mn);
             s_m[ts] = mn;
           }
@@ -528,29 +488,31 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
           }
         }
         if (puse > 0) ok = ok && pv_wait(pl.np);         // the buffer's last values are done
-        uint32_t pk[kG][2];                              // rows c0, c0 + 1 of tokens tok, tok + 8
+        if (act) {
+          uint32_t pk[kG][2];                              // rows c0, c0 + 1 of tokens tok, tok + 8
 #pragma unroll
-        for (int i = 0; i < kG; ++i) {
-          float x[4];
+          for (int i = 0; i < kG; ++i) {
+            float x[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            x[e] = ex2(fmaf(__uint_as_float(s[i][e]), c, -m[i][e & 1]));
-          l[i][0] += x[0] + x[2];
-          l[i][1] += x[1] + x[3];
-          pk[i][0] = pack_bf16(x[0], x[1]);
-          pk[i][1] = pack_bf16(x[2], x[3]);
+            for (int e = 0; e < 4; ++e)
+              x[e] = ex2(fmaf(__uint_as_float(s[i][e]), c, -m[i][e & 1]));
+            l[i][0] += x[0] + x[2];
+            l[i][1] += x[1] + x[3];
+            pk[i][0] = pack_bf16(x[0], x[1]);
+            pk[i][1] = pack_bf16(x[2], x[3]);
+          }
+          // to shared memory two groups of rows at once: lane 8 k + j addresses row j of matrix k,
+          // tokens [8 (k % 2), + 8) of group i + k / 2
+          const uint32_t pr = smem_u32(sp + pb * pl.p_bytes);
+          const uint32_t at = 16 * wq + (lane & 15);
+#pragma unroll
+          for (int i = 0; i + 1 < kG; i += 2)
+            stmatrix_x4(pr + chunk_mnmajor_sw32(g0 + i + (lane >> 4), at, KT), pk[i][0],
+                        pk[i][1], pk[i + 1][0], pk[i + 1][1]);
+          if (kG & 1)
+            stmatrix_x2(pr + chunk_mnmajor_sw32(g0 + kG - 1, at, KT), pk[kG - 1][0],
+                        pk[kG - 1][1]);
         }
-        // to shared memory two groups of rows at once: lane 8 k + j addresses row j of matrix k,
-        // tokens [8 (k % 2), + 8) of group i + k / 2
-        const uint32_t pr = smem_u32(sp + pb * pl.p_bytes);
-        const uint32_t at = 16 * wq + (lane & 15);
-#pragma unroll
-        for (int i = 0; i + 1 < kG; i += 2)
-          stmatrix_x4(pr + chunk_mnmajor_sw32(g0 + i + (lane >> 4), at, kTcTile), pk[i][0],
-                      pk[i][1], pk[i + 1][0], pk[i + 1][1]);
-        if (kG & 1)
-          stmatrix_x2(pr + chunk_mnmajor_sw32(g0 + kG - 1, at, kTcTile), pk[kG - 1][0],
-                      pk[kG - 1][1]);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.p_full[pb]);
@@ -563,20 +525,28 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
       // ---- results: whole blocks to the output, shared ones to a partial slot
       const bool first = p.t0 == 0, last = p.t1 == p.tiles;
       const int slot = first && last ? -1 : 2 * (int)blockIdx.x + (first ? 1 : 0);
+      auto sums = [&](bool with) {
 #pragma unroll
-      for (int i = 0; i < kG; ++i) {
+        for (int i = 0; i < kG; ++i) {
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) {
             l[i][0] += __shfl_xor_sync(kAll, l[i][0], o);
             l[i][1] += __shfl_xor_sync(kAll, l[i][1], o);
           }
-          if (lane < 4)
-            *reinterpret_cast<float2*>(&s_red[wq][8 * (g0 + i) + c0]) = make_float2(l[i][0], l[i][1]);
+          float* d = s_red + (wq & 1) * nr + 8 * (g0 + i) + c0;
+          if (lane < 4) {
+            d[0] = with ? l[i][0] + d[0] : l[i][0];
+            d[1] = with ? l[i][1] + d[1] : l[i][1];
+          }
         }
+      };
+      if (wq < 2) sums(false);
+      named_bar(1, kSoft);
+      if (wq >= 2 && act) sums(true);
       ok = ok && pv_wait(1);
       if (named_bar_or(1, kSoft, !ok)) break;
       if (ts < nr) {
-        const float z = (s_red[0][ts] + s_red[1][ts]) + (s_red[2][ts] + s_red[3][ts]);
+        const float z = s_red[ts] + s_red[nr + ts];
         s_row[ts] = z == 0.f ? 0.f : 1.0f / z;
         const float y = z == 0.f ? -INFINITY : s_m[ts] * kLn2 + logf(z);
         if (slot >= 0) pt.lse[slot * nr + ts] = y;
@@ -643,7 +613,7 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
   }
 }
 
-using TcKernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, const int32_t*, const int32_t*,
+using TcKernel = void (*)(CUtensorMap, CUtensorMap, const int32_t*, const int32_t*,
                           const int32_t*, bf16*, float*, LatentAttnShape, TcPlan, LatentPartials);
 TcKernel tc_kernel(int nr) {
   switch (nr) {
@@ -656,12 +626,12 @@ TcKernel tc_kernel(int nr) {
   }
 }
 
-// Rows of a block: all of a sequence's where they fit, else the size that cuts them into
-// fewer blocks (each reads the cached rows again), the smaller one where both do.
+// Rows of a block: all of a sequence's up to 96, a multiple of 16; of more, 64, whose tiles of
+// 64 tokens cost the MMAs less a row and token than 96 with tiles of 48 (a 1024-token chunk
+// of 12 heads behind 8192 to 32768 tokens: 562 us against 635).
 int tc_rows(int N, int L, int T, int H) {
   const long long rows = L > 0 ? (long long)L * H : (((long long)T + N - 1) / N) * H;
-  if (rows <= kTcMaxRows) return (int)((rows + 15) / 16 * 16);
-  return (rows + 63) / 64 <= (rows + kTcMaxRows - 1) / kTcMaxRows ? 64 : kTcMaxRows;
+  return rows <= kTcMaxRows ? (int)((rows + 15) / 16 * 16) : 64;
 }
 
 }  // namespace
@@ -681,28 +651,25 @@ cudaError_t launch_latent_tc(const void* q, const void* cache, const int32_t* pa
   if (!once_per_device(kOnceLatentTc, []() {
         for (int nr = 16; nr <= kTcMaxRows; nr += 16)
           if (cudaFuncSetAttribute(tc_kernel(nr), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                   (int)kTcSmem) != cudaSuccess)
+                                   (int)tc_smem(nr)) != cudaSuccess)
             return false;
         return true;
       }))
     return cudaErrorInvalidDevice;
   const int nr = tc_rows(sh.N, sh.L, sh.T, sh.H), G = latent_tc_ctas(sms);
-  const TcPlan pl = tc_plan(nr, sh.rank, sh.rope, sh.page_size);
+  const TcPlan pl = tc_plan(nr, sh.rank, sh.rope);
   const LatentPartials pt = latent_partials(buf, G, nr);
   const uint64_t D = sh.rank + sh.rope;
   const uint64_t rows = (uint64_t)(sh.L > 0 ? (long long)sh.N * sh.L : sh.T) * sh.H;
-  CUtensorMap q_map, c_map, r_map;
-  const auto cache_map = [&](CUtensorMap* m, uint32_t chunks) {
-    return make_chunk_map_4d(m, cache, sh.page_size, D / 64, sh.num_pages, sh.row_stride * 2,
-                             sh.page_stride * 2, (uint32_t)pl.box_rows, chunks);
-  };
+  CUtensorMap q_map, c_map;
   if (!make_chunk_map_4d(&q_map, q, rows, D / 64, 1, D * 2, D * 2, (uint32_t)nr,
                          (uint32_t)(D / 64)) ||
-      !cache_map(&c_map, 2) || !cache_map(&r_map, 1))
+      !make_chunk_map_4d(&c_map, cache, sh.page_size, D / 64, sh.num_pages, sh.row_stride * 2,
+                         sh.page_stride * 2, 8, (uint32_t)(D / 64)))
     return cudaErrorInvalidValue;
   KDA_TIMED(KDA_KERNEL_LATENT_ATTN, stream,
-            tc_kernel(nr)<<<G, kTcThreads, kTcSmem, stream>>>(
-                q_map, c_map, r_map, page_table, seq_lens, cu_seqlens, static_cast<bf16*>(out), lse, sh,
+            tc_kernel(nr)<<<G, kTcThreads, tc_smem(nr), stream>>>(
+                q_map, c_map, page_table, seq_lens, cu_seqlens, static_cast<bf16*>(out), lse, sh,
                 pl, pt));
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
