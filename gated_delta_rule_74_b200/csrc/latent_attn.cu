@@ -230,9 +230,9 @@ kda_latent_simt_kernel(const T* __restrict__ q, const T* __restrict__ cache,
 
 // ---------------------------------------------------------------------------
 // Join: row = sum_c e^(lse_c - M) o_c / sum_c e^(lse_c - M) over the CTAs that share the
-// row's block, in their order.  Bound by latency (the partial results are in L2): a block's
-// four groups of 128 threads take a row each while few CTAs share it, all loads at once,
-// and a quarter of the CTAs each where many do.
+// row's block, in their order.  Bound by latency (the partial results are in L2).  While few
+// CTAs share a row, a group of 128 threads takes it, all loads at once; where many do, a block
+// takes 128 of its columns, each of its 16 warps a sixteenth of the CTAs.
 constexpr int kJT = 512;
 constexpr int kFew = 8;
 
@@ -263,8 +263,8 @@ __global__ void __launch_bounds__(kJT)
 kda_latent_join_kernel(T* __restrict__ out, float* __restrict__ lse, LatentPartials pt, int G,
                        int nr, int rank, bool list) {
   __shared__ float s_w[kLatentMaxCtas];
-  __shared__ float4 s_part[3][128];
-  const int tid = threadIdx.x, lane = tid & 31;
+  __shared__ float4 s_part[kJT / 32][32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = tid >> 7, d4 = tid & 127;
   __shared__ int s_list[kLatentMaxCtas], s_n;
   __shared__ uint32_t s_mask[kLatentMaxCtas / 32];
@@ -319,17 +319,19 @@ kda_latent_join_kernel(T* __restrict__ out, float* __restrict__ lse, LatentParti
     return;
   }
   const int u0 = list ? blockIdx.x : blockIdx.y, du = list ? gridDim.x : gridDim.y;
-  const int units = list ? s_n * nr : hd.y;
+  const int parts = rank / 128;                        // units of a row
+  const int units = (list ? s_n * nr : hd.y) * parts;
   for (int u = u0; u < units; u += du) {
-    int r = u;
+    int r = u / parts;
+    const int d = 128 * (u - r * parts) + 4 * lane;
     if (list) {
-      c0 = s_list[u / nr];
-      r = u % nr;
+      c0 = s_list[r / nr];
+      r %= nr;
       hd = pt.head[c0];
       k = hd.z - c0 + 1;
       if (r >= hd.y) continue;
     }
-    __syncthreads();                                   // s_w and s_part of the row before are read
+    __syncthreads();                                   // s_w and s_part of the unit before are read
     for (int i = tid; i < k; i += kJT) s_w[i] = pt.lse[join_slot(c0, i) * nr + r];
     __syncthreads();
     float M = -INFINITY;
@@ -338,31 +340,28 @@ kda_latent_join_kernel(T* __restrict__ out, float* __restrict__ lse, LatentParti
     for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     const float Ms = M == -INFINITY ? 0.f : M;
     float z = 0.f;
-    for (int i = lane; i < k; i += 32) z += expf(s_w[i] - Ms);
+    for (int i = lane; i < k; i += 32) z += expf(s_w[i] - Ms);   // a NaN makes all of it one
 #pragma unroll
     for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
     const float inv = z == 0.f ? 0.f : 1.0f / z;
-    if (tid == 0 && lse) lse[hd.x + r] = z == 0.f ? -INFINITY : Ms + logf(z);
-    const int i0 = k * g / 4, i1 = k * (g + 1) / 4;
+    if (tid == 0 && d == 0 && lse) lse[hd.x + r] = z == 0.f ? -INFINITY : Ms + logf(z);
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (d4 * 4 < rank) {
-#pragma unroll 8
-      for (int i = i0; i < i1; ++i)
-        join_add(a, expf(s_w[i] - Ms) * inv,
-                 *reinterpret_cast<const float4*>(pt.o + (join_slot(c0, i) * nr + r) * rank + d4 * 4));
-    }
-    if (g > 0) s_part[g - 1][d4] = a;
+#pragma unroll 4
+    for (int i = warp; i < k; i += kJT / 32)
+      join_add(a, expf(s_w[i] - Ms) * inv,
+               *reinterpret_cast<const float4*>(pt.o + (join_slot(c0, i) * nr + r) * rank + d));
+    s_part[warp][lane] = a;
     __syncthreads();
-    if (g == 0 && d4 * 4 < rank) {
+    if (warp == 0) {
 #pragma unroll
-      for (int i = 0; i < 3; ++i) {
-        const float4 v = s_part[i][d4];
+      for (int i = 1; i < kJT / 32; ++i) {
+        const float4 v = s_part[i][lane];
         a.x += v.x;
         a.y += v.y;
         a.z += v.z;
         a.w += v.w;
       }
-      join_store(out + (long long)(hd.x + r) * rank + d4 * 4, a);
+      join_store(out + (long long)(hd.x + r) * rank + d, a);
     }
   }
 }
