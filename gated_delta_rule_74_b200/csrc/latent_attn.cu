@@ -230,11 +230,11 @@ kda_latent_simt_kernel(const T* __restrict__ q, const T* __restrict__ cache,
 
 // ---------------------------------------------------------------------------
 // Join: row = sum_c e^(lse_c - M) o_c / sum_c e^(lse_c - M) over the CTAs that share the
-// row's block, in their order.  Bound by latency (the partial results are in L2).  While few
-// CTAs share a row, a group of 128 threads takes it, all loads at once; where many do, a block
-// takes 128 of its columns, each of its 16 warps a sixteenth of the CTAs.
+// row's block, in their order.  Bound by latency (the partial results are in L2).  Up to 8 CTAs
+// a row: 128 threads take it, all loads at once; up to 64: a warp takes 128 of its columns,
+// eight loads at a time; more: a block does, each of its 16 warps a sixteenth of the CTAs.
 constexpr int kJT = 512;
-constexpr int kFew = 8;
+constexpr int kFew = 8, kSome = 64;
 
 // Partial slot of the i-th CTA of a shared block that starts in CTA c0.
 __device__ __forceinline__ long long join_slot(int c0, int i) {
@@ -318,8 +318,38 @@ kda_latent_join_kernel(T* __restrict__ out, float* __restrict__ lse, LatentParti
     }
     return;
   }
-  const int u0 = list ? blockIdx.x : blockIdx.y, du = list ? gridDim.x : gridDim.y;
   const int parts = rank / 128;                        // units of a row
+  if (!list && k <= kSome) {
+    constexpr int kWarps = kJT / 32;
+    for (int u = blockIdx.y * kWarps + warp; u < hd.y * parts; u += gridDim.y * kWarps) {
+      const int r = u / parts, d = 128 * (u - r * parts) + 4 * lane;
+      float w[2];                                      // of CTAs lane, lane + 32
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        w[j] = lane + 32 * j < k ? pt.lse[join_slot(c0, lane + 32 * j) * nr + r] : -INFINITY;
+      float M = fmaxf(w[0], w[1]);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+      const float Ms = M == -INFINITY ? 0.f : M;
+      w[0] = expf(w[0] - Ms);                          // a NaN makes all of it one
+      w[1] = expf(w[1] - Ms);
+      float z = w[0] + w[1];
+#pragma unroll
+      for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+      const float inv = z == 0.f ? 0.f : 1.0f / z;
+      if (d == 0 && lse) lse[hd.x + r] = z == 0.f ? -INFINITY : Ms + logf(z);
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll 8
+        for (int i = 32 * j; i < min(k, 32 * j + 32); ++i)
+          join_add(a, __shfl_sync(0xffffffffu, w[j], i & 31) * inv,
+                   *reinterpret_cast<const float4*>(pt.o + (join_slot(c0, i) * nr + r) * rank + d));
+      join_store(out + (long long)(hd.x + r) * rank + d, a);
+    }
+    return;
+  }
+  const int u0 = list ? blockIdx.x : blockIdx.y, du = list ? gridDim.x : gridDim.y;
   const int units = (list ? s_n * nr : hd.y) * parts;
   for (int u = u0; u < units; u += du) {
     int r = u / parts;
@@ -408,8 +438,8 @@ int simt_ctas(int sms) { return 2 * sms < kLatentMaxCtas ? 2 * sms : kLatentMaxC
 // `items`: blocks of rows of the call (packed: about).  Few of them are spread over the rows.
 cudaError_t launch_latent_join(void* out, float* lse, const LatentPartials& pt, int G, int nr,
                                int rank, long long items, int dtype, cudaStream_t stream) {
-  const bool list = items <= 16;
-  const dim3 grid = list ? dim3(2 * G) : dim3(G, (nr + 3) / 4);
+  const bool list = items * kSome <= G;                // each is shared by more than kSome CTAs
+  const dim3 grid = list ? dim3(4 * G) : dim3(G, nr <= 32 ? 4 : (nr + 7) / 8);
   cudaError_t e = cudaSuccess;
   if (dtype == KDA_BF16)
     KDA_TIMED(KDA_KERNEL_LATENT_ATTN, stream,
