@@ -55,7 +55,7 @@ constexpr int kMaxTiles = 4;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kWaitLimit = 1u << 22, kPollLimit = 1u << 26, kDrainLimit = 1u << 14;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kNone = -1e30f;                    // maximum of a row that has seen nothing
+constexpr float kNone = -3e38f;                    // maximum of a row that has seen nothing
 
 // Tokens of a tile.  64 fill the MMAs' M side; 48 where only one tile of 64 would fit beside Q
 // (148 sequences of 8192 tokens and 96 heads: 401 us against 419 with one and a half).  At 48

@@ -112,11 +112,12 @@ def test_attn_rows_that_see_nothing(dtype, lens, L):
         assert bool((lse[n, :max(L - t, 0)] == -math.inf).all())
 
 
-@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dtype,L,H", [("bf16", 6, 12), ("bf16", 3, 4), ("bf16", 4, 40), ("bf16", 3, 32),
+                                       ("f32", 6, 12)])
 @pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
-def test_attn_hidden_rows_have_no_effect(dtype, bad):
+def test_attn_hidden_rows_have_no_effect(dtype, L, H, bad):
     """NaN and infinities behind the length, in unused pages and in later new tokens."""
-    L, H, page = 6, 12, 16
+    page = 16
     x = make(dtype, [70, 6, 33], L, H, 512, 64, page)
     good = ref.attend(x["q"], x["cache"], x["table"], x["lens"], x["rank"], x["scale"])
     seen = torch.zeros(x["cache"].shape[:2], dtype=torch.bool)
@@ -130,10 +131,11 @@ def test_attn_hidden_rows_have_no_effect(dtype, bad):
         close(y, out[n:n + 1, :L - 2], lse[n:n + 1, :L - 2], tuple(t[n:n + 1, :L - 2] for t in good))
 
 
-@pytest.mark.parametrize("dtype", ["bf16", "f32"])
-def test_attn_large_scores_and_far_maximum(dtype):
+@pytest.mark.parametrize("dtype,H", [("bf16", 5), ("bf16", 12), ("bf16", 30), ("bf16", 48), ("bf16", 60),
+                                     ("f32", 12)])
+def test_attn_large_scores_and_far_maximum(dtype, H):
     """Scores of hundreds, the largest one late: the running maximum has to move."""
-    x = make(dtype, [500, 257], 2, 12, 256, 64, 64, spread=20.0)
+    x = make(dtype, [500, 257], 2, H, 256, 64, 64, spread=20.0)
     pos = x["table"][0, 480 // 64], 480 % 64
     x["cache"][pos] = x["q"][0, 0, 0] / 4
     close(x, *call(x))
@@ -166,13 +168,58 @@ def test_attn_lengths_and_pages_out_of_range_stay_inside(dtype):
     assert bool((out[1] == 0).all())
 
 
-def test_attn_long_sequence_is_split_and_joined():
-    """One sequence over all SMs, and the same bits again."""
-    x = make("bf16", [9000], 1, 12, 512, 64, 64)
+@pytest.mark.parametrize("dtype,lens,H,rank,page", [
+    ("bf16", [9000], 12, 512, 64), ("bf16", [9500], 96, 512, 64), ("bf16", [5000, 40, 7000], 30, 384, 16),
+    ("bf16", [900] * 9 + [1], 12, 128, 64), ("bf16", [9000, 100, 200, 300, 50, 60], 96, 256, 64),
+    ("f32", [5000], 12, 256, 64), ("f32", [300] * 20, 3, 128, 64)])
+def test_attn_long_sequence_is_split_and_joined(dtype, lens, H, rank, page):
+    """One sequence or a few over all SMs, by few, some and many CTAs; and the same bits again."""
+    x = make(dtype, lens, 1, H, rank, 64, page)
     out, lse = call(x)
     close(x, out, lse)
     again = call(x)
     assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
+@pytest.mark.parametrize("dtype,page", [("bf16", 16), ("bf16", 9), ("f32", 16)])
+def test_attn_shared_pages(dtype, page):
+    """Sequences that share their first pages, and one that is another's twin."""
+    x = make(dtype, [100, 90, 100, 33], 2, 12, 256, 64, page)
+    share = 32 // page
+    x["table"][1, :share] = x["table"][0, :share]
+    x["table"][2] = x["table"][0]
+    x["q"][2] = x["q"][0]
+    out, lse = call(x)
+    close(x, out, lse)
+    assert torch.equal(lse[0], lse[2])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_attn_packed_without_tokens(dtype):
+    x = make(dtype, [10, 0], 6, 3, 128, 64, 16, cu=[0, 0, 0])
+    out = torch.full((1, 6, 3, 128), 7.0, dtype=DT[dtype], device="cuda")
+    lse = torch.full((1, 6, 3), 7.0, device="cuda")
+    call(x, out=out, lse=lse)
+    assert bool((out == 7.0).all()) and bool((lse == 7.0).all())
+
+
+@pytest.mark.parametrize("dtype,page", [("bf16", 64), ("bf16", 60), ("f32", 64)])
+def test_offsets_beyond_32_bits(dtype, page):
+    """The last pages of a cache of more than 2^31 elements (and 2^32 bytes)."""
+    x = make(dtype, [150, 20], 2, 12, 512, 64, page)
+    P = x["cache"].shape[0]
+    total = 2 ** 31 // (page * 576) + P + 1
+    big = torch.empty((total, page, 576), dtype=DT[dtype], device="cuda")
+    big[total - P:] = x["cache"].cuda()
+    y = dict(x, table=torch.where(x["table"] >= 0, x["table"] + (total - P), x["table"]))
+    out, lse = call(y, cache=big)
+    close(x, out, lse)
+    kv = torch.randn((2, 2, 576)).to(DT[dtype])
+    kda.kda_latent_append(kv.cuda(), big, y["table"].cuda(), y["lens"].cuda(), rank=512)
+    for n, t in enumerate((150, 20)):
+        for i in (1, 2):
+            pos = t - i
+            assert torch.equal(big[int(y["table"][n, pos // page]), pos % page].cpu(), kv[n, 2 - i])
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
