@@ -252,17 +252,16 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
-# The current stream's handle without a Stream object around it: 0.07 us a call, not 3.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# The current stream's handle without a Stream object around it (0.07 us a call, not 3), and
+# the current device without the check that CUDA is up.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream) -> int:
     """Handle of `stream`, by default of the current device's current stream."""
-    if stream is not None:
-        return stream.cuda_stream
-    if _raw_stream is not None:
-        return _raw_stream(torch.cuda.current_device())
-    return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(torch.cuda.current_device()) if stream is None else stream.cuda_stream
 
 
 def _check(name: str, t: torch.Tensor, dtype=None, shape=None):
@@ -567,20 +566,20 @@ def kda_decode_chunk(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch
 
 def _run_on(dev: int, stream, fn, args, name: str) -> None:
     """fn(*args, stream handle) with device `dev` current (the library works on that one)."""
-    if dev != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            rc = fn(*args, _stream(stream))
+    handle = _raw_stream(dev) if stream is None else stream.cuda_stream
+    if dev == _current_device():
+        rc = fn(*args, handle)
     else:
-        rc = fn(*args, _stream(stream))
+        with torch.cuda.device(dev):
+            rc = fn(*args, handle)
     if rc != KDA_OK:
         raise KdaError(name, rc)
 
 
 def _device_of(name: str, t: torch.Tensor) -> int:
-    dev = t.get_device()
-    if dev < 0 or not t.is_cuda:
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return dev
+    return t.get_device()
 
 
 def _take(name: str, t: Optional[torch.Tensor], dev: int, dtype, shape) -> Optional[int]:
@@ -588,30 +587,30 @@ def _take(name: str, t: Optional[torch.Tensor], dev: int, dtype, shape) -> Optio
     decode step's calls are as short as their checks."""
     if t is None:
         return None
-    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-        _check(name, t, dtype, shape)
-        raise ValueError(f"{name} is on {t.device}, the call's other tensors on cuda:{dev}")
-    return t.data_ptr()
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
+        return t.data_ptr()
+    _check(name, t, dtype, shape)
+    raise ValueError(f"{name} is on {t.device}, the call's other tensors on cuda:{dev}")
 
 
 def _latent_args(B: int, T: int, D: int, dtype, dev: int, kv_cache: torch.Tensor,
                  page_table: torch.Tensor, seq_lens: torch.Tensor,
                  cu_seqlens: Optional[torch.Tensor], rank: int):
-    """Checks shared by kda_latent_append and kda_latent_attn: (dtype id, the pointers of
-    cache, table, lengths and offsets, sequences, cache and table sizes and strides)."""
+    """Checks shared by kda_latent_append and kda_latent_attn: (the pointers of cache, table,
+    lengths and offsets), sequences, (cache and table sizes and strides), dtype id."""
     dt = _DTYPES.get(dtype)
     if dt is None:
         raise ValueError(f"unsupported dtype {dtype}")
     if not 0 < rank <= D:
         raise ValueError(f"rank {rank} does not fit rows of {D}")
-    if kv_cache.dim() != 3 or kv_cache.shape[2] != D or kv_cache.dtype is not dtype:
+    shape = kv_cache.shape
+    if len(shape) != 3 or shape[2] != D or kv_cache.dtype is not dtype:
         raise ValueError(f"kv_cache must be [pages, page_size, {D}] of {dtype}, got "
-                         f"{tuple(kv_cache.shape)} of {kv_cache.dtype}")
+                         f"{tuple(shape)} of {kv_cache.dtype}")
     page_stride, row_stride, one = kv_cache.stride()
-    if kv_cache.get_device() != dev or one != 1:
+    if one != 1 or kv_cache.get_device() != dev:
         raise ValueError(f"kv_cache must be a tensor on cuda:{dev} with contiguous rows")
     nseq = seq_lens.numel()
-    lens = _take("seq_lens", seq_lens, dev, torch.int32, (nseq,))
     cu = None
     if cu_seqlens is not None:
         cu = _take("cu_seqlens", cu_seqlens, dev, torch.int32, (nseq + 1,))
@@ -619,24 +618,32 @@ def _latent_args(B: int, T: int, D: int, dtype, dev: int, kv_cache: torch.Tensor
             raise ValueError("packed inputs (cu_seqlens) must have B == 1")
     elif nseq != B:
         raise ValueError(f"seq_lens has {nseq} entries for {B} sequences")
-    if page_table.dim() != 2:
-        raise ValueError(f"page_table must be [{nseq}, max_pages], got {tuple(page_table.shape)}")
-    most = page_table.shape[1]
-    table = _take("page_table", page_table, dev, torch.int32, (nseq, most))
-    pages, page_size, _ = kv_cache.shape
-    return (dt, kv_cache.data_ptr(), table, lens, cu, nseq,
-            (pages, page_size, most, page_stride, row_stride))
+    most = page_table.shape[-1] if page_table.dim() == 2 else -1
+    return ((kv_cache.data_ptr(), _take("page_table", page_table, dev, torch.int32, (nseq, most)),
+             _take("seq_lens", seq_lens, dev, torch.int32, (nseq,)), cu), nseq,
+            (shape[0], shape[1], most, page_stride, row_stride), dt)
 
 
 def _token_stride(name: str, t: torch.Tensor, dense: int) -> int:
     """Elements from one token of t [B, T, ..] to the next, which has to hold across B
     (`dense` where there is but one token)."""
-    B, T = t.shape[:2]
+    (B, T), s = t.shape[:2], t.stride()
     if T > 1:
-        if B > 1 and t.stride(0) != T * t.stride(1):
+        if B > 1 and s[0] != T * s[1]:
             raise ValueError(f"{name}'s sequences must follow each other at its token stride")
-        return t.stride(1)
-    return t.stride(0) if B > 1 else dense
+        return s[1]
+    return s[0] if B > 1 else dense
+
+
+def _position_values(name: str, t: torch.Tensor, shape, dtype, dev: int):
+    """Pointer, token stride and head stride of the queries' position values."""
+    if t.shape != shape or t.dtype is not dtype:
+        raise ValueError(f"{name} must be {list(shape)} of {dtype}, got {tuple(t.shape)} of {t.dtype}")
+    s = t.stride()
+    if s[3] != 1 or t.get_device() != dev:
+        raise ValueError(f"{name} must be a tensor on cuda:{dev} with contiguous rows")
+    H, rope = shape[2:]
+    return t.data_ptr(), _token_stride(name, t, H * rope), s[2] if H > 1 else rope
 
 
 def kda_latent_append(kv: torch.Tensor, kv_cache: torch.Tensor, page_table: torch.Tensor,
@@ -656,32 +663,24 @@ def kda_latent_append(kv: torch.Tensor, kv_cache: torch.Tensor, page_table: torc
     if kv.dim() != 3:
         raise ValueError("kv must be [B, T, rank + rope]")
     B, T, D = kv.shape
-    dev = _device_of("kv", kv)
-    dt, cache, table, lens, cu, nseq, (pages, page_size, most, page_stride, row_stride) = \
-        _latent_args(B, T, D, kv.dtype, dev, kv_cache, page_table, seq_lens, cu_seqlens, rank)
-    rope = D - rank
+    dev, dtype, rope = _device_of("kv", kv), kv.dtype, D - rank
+    ptrs, nseq, sizes, dt = _latent_args(B, T, D, dtype, dev, kv_cache, page_table, seq_lens,
+                                         cu_seqlens, rank)
     if kv.stride(2) != 1:
         raise ValueError("kv must have contiguous rows")
-    H, qs = 1, (0, 0, 0, 0)
+    H, qp, qt, qh, op, ot, oh = 1, None, 0, 0, None, 0, 0
     if q_pe is not None:
         if q_pe_out is None:
             q_pe_out = torch.empty(q_pe.shape, dtype=q_pe.dtype, device=q_pe.device)
         H = q_pe.shape[2] if q_pe.dim() == 4 else 0
-        for name, t in (("q_pe", q_pe), ("q_pe_out", q_pe_out)):
-            if t.shape != (B, T, H, rope) or t.dtype is not kv.dtype:
-                raise ValueError(f"{name} must be [{B}, {T}, H, {rope}] of {kv.dtype}, got "
-                                 f"{tuple(t.shape)} of {t.dtype}")
-            if t.get_device() != dev or t.stride(3) != 1:
-                raise ValueError(f"{name} must be a tensor on cuda:{dev} with contiguous rows")
-        qs = (_token_stride("q_pe", q_pe, H * rope), q_pe.stride(2) if H > 1 else rope,
-              _token_stride("q_pe_out", q_pe_out, H * rope), q_pe_out.stride(2) if H > 1 else rope)
+        qp, qt, qh = _position_values("q_pe", q_pe, (B, T, H, rope), dtype, dev)
+        op, ot, oh = _position_values("q_pe_out", q_pe_out, (B, T, H, rope), dtype, dev)
     elif q_pe_out is not None:
         raise ValueError("q_pe_out needs q_pe")
     _run_on(dev, stream, lib().kda_latent_append,
             (kv.data_ptr(), _take("norm_weight", norm_weight, dev, torch.float32, (rank,)),
-             _take("inv_freq", inv_freq, dev, torch.float32, (rope // 2,)), _ptr(q_pe),
-             _ptr(q_pe_out), cache, table, lens, cu, nseq, T, H, rank, rope, pages, page_size, most,
-             page_stride, row_stride, _token_stride("kv", kv, D), *qs, eps, interleaved, dt),
+             _take("inv_freq", inv_freq, dev, torch.float32, (rope // 2,)), qp, op, *ptrs, nseq, T, H,
+             rank, rope, *sizes, _token_stride("kv", kv, D), qt, qh, ot, oh, eps, interleaved, dt),
             "kda_latent_append")
     return q_pe_out
 
@@ -714,18 +713,22 @@ def kda_latent_attn(q: torch.Tensor, kv_cache: torch.Tensor, page_table: torch.T
     if q.dim() != 4:
         raise ValueError("q must be [B, T, H, rank + rope]")
     B, T, H, D = q.shape
-    dev = _device_of("q", q)
+    dev, dtype = _device_of("q", q), q.dtype
     if not q.is_contiguous():
         raise ValueError("q must be contiguous")
-    dt, cache, table, lens, cu, nseq, (pages, page_size, most, page_stride, row_stride) = \
-        _latent_args(B, T, D, q.dtype, dev, kv_cache, page_table, seq_lens, cu_seqlens, rank)
+    ptrs, nseq, sizes, dt = _latent_args(B, T, D, dtype, dev, kv_cache, page_table, seq_lens,
+                                         cu_seqlens, rank)
     if out is None:
         out = q.new_empty((B, T, H, rank))
+        op = out.data_ptr()
+    else:
+        op = _take("out", out, dev, dtype, (B, T, H, rank))
     if lse is None:
         lse = torch.empty((B, T, H), dtype=torch.float32, device=q.device)
-    args = (q.data_ptr(), cache, table, lens, cu, _take("out", out, dev, q.dtype, (B, T, H, rank)),
-            _take("lse", lse, dev, torch.float32, (B, T, H)), nseq, T, H, rank, D - rank, pages,
-            page_size, most, page_stride, row_stride, scale, dt)
+        lp = lse.data_ptr()
+    else:
+        lp = _take("lse", lse, dev, torch.float32, (B, T, H))
+    args = (q.data_ptr(), *ptrs, op, lp, nseq, T, H, rank, D - rank, *sizes, scale, dt)
     if workspace is not None:
         if workspace.get_device() != dev:
             raise ValueError(f"workspace must be on cuda:{dev}")
@@ -751,16 +754,21 @@ def kda_verify_tokens(target: torch.Tensor, draft: Optional[torch.Tensor],
     N, L1, V = target.shape
     L = L1 - 1
     dev = _device_of("target", target)
+    xp = _take("draft_tokens", draft_tokens, dev, torch.int32, (N, L))
     if tokens is None:
         tokens = draft_tokens.new_empty((N, L1))
+        tp = tokens.data_ptr()
+    else:
+        tp = _take("tokens", tokens, dev, torch.int32, (N, L1))
     if accepted is None:
         accepted = draft_tokens.new_empty((N,))
+        ap = accepted.data_ptr()
+    else:
+        ap = _take("accepted", accepted, dev, torch.int32, (N,))
     _run_on(dev, stream, lib().kda_verify_tokens,
             (_take("target", target, dev, torch.float32, (N, L1, V)),
-             _take("draft", draft, dev, torch.float32, (N, L, V)),
-             _take("draft_tokens", draft_tokens, dev, torch.int32, (N, L)),
+             _take("draft", draft, dev, torch.float32, (N, L, V)), xp,
              _take("uniforms", uniforms, dev, torch.float32, (N, L1)),
-             _take("draft_lens", draft_lens, dev, torch.int32, (N,)),
-             _take("tokens", tokens, dev, torch.int32, (N, L1)),
-             _take("accepted", accepted, dev, torch.int32, (N,)), N, L, V), "kda_verify_tokens")
+             _take("draft_lens", draft_lens, dev, torch.int32, (N,)), tp, ap, N, L, V),
+            "kda_verify_tokens")
     return tokens, accepted
