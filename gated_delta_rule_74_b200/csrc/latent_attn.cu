@@ -25,6 +25,7 @@ namespace {
 constexpr int kNT = 256;
 constexpr int kRows = 16;                // rows of a block
 constexpr int kTile = 32;                // cached rows of a tile
+constexpr int kLead = 1;                 // tiles that a block costs besides its own
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // Four neighbouring elements as fp32.
@@ -76,7 +77,7 @@ kda_latent_simt_kernel(const T* __restrict__ q, const T* __restrict__ cache,
   __shared__ LatentStart st;
   __shared__ long long s_sum[33];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  latent_find_start(sh, seq_lens, cu_seqlens, kRows, kTile, &st, s_sum);
+  latent_find_start(sh, seq_lens, cu_seqlens, kRows, kTile, kLead, &st, s_sum);
   if (tid == 0) pt.head[blockIdx.x] = make_int4(0, 0, 0, 0);
 
   constexpr int E = 16 / sizeof(T);
@@ -85,7 +86,7 @@ kda_latent_simt_kernel(const T* __restrict__ q, const T* __restrict__ cache,
   const int hr = 8 * (tid & 1), d0 = (tid >> 1) * kD;       // output: rows hr .., columns d0 ..
   LatentWalk walk(st);
   LatentPiece p;
-  while (walk.next(sh, seq_lens, cu_seqlens, kRows, kTile, &p)) {
+  while (walk.next(sh, seq_lens, cu_seqlens, kRows, kTile, kLead, &p)) {
     // tile t into buffer b, eight threads a row; zeros where there is no row
     auto fetch = [&](int t, int b) {
       const int row = tid >> 3, pos = t * kTile + row;
@@ -213,7 +214,7 @@ kda_latent_simt_kernel(const T* __restrict__ q, const T* __restrict__ cache,
     }
     if (slot >= 0 && first && tid == 0)
       pt.head[blockIdx.x] =
-          make_int4((int)p.row0, p.rows, latent_cta_of(p.pos + p.tiles - 1, st.W, st.G), 0);
+          make_int4((int)p.row0, p.rows, latent_cta_of(p.end, st.W, st.G), 0);
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 8; ++i) {

@@ -114,38 +114,39 @@ struct LatentSeq {
   }
   // Tiles of block b: its last row's limit is len - cnt + (b nr + nr - 1) / H + 1, so that
   // ceil(limit / kt) = floor((b nr + base) / (kt H)); one at least.
-  __device__ int cost(int b, const LatentAttnShape& sh, int nr, int kt) const {
+  __device__ int tiles(int b, const LatentAttnShape& sh, int nr, int kt) const {
     if (b == nb - 1) return max(1, (len + kt - 1) / kt);
     return b < b1 ? 1 : (int)(((long long)b * nr + base) / ((long long)kt * sh.H));
   }
-  // Tiles of blocks [0, b), b < nb
-  __device__ long long before(int b, const LatentAttnShape& sh, int nr, int kt) const {
-    if (b <= b1) return b;
-    return b1 + floor_sum(b - b1, (long long)kt * sh.H, nr, base + (long long)nr * b1);
+  // Places of blocks [0, b), b < nb
+  __device__ long long before(int b, const LatentAttnShape& sh, int nr, int kt, int lead) const {
+    const long long n = (long long)b * lead;
+    if (b <= b1) return n + b;
+    return n + b1 + floor_sum(b - b1, (long long)kt * sh.H, nr, base + (long long)nr * b1);
   }
-  __device__ long long total(const LatentAttnShape& sh, int nr, int kt) const {
-    return nb == 0 ? 0 : before(nb - 1, sh, nr, kt) + cost(nb - 1, sh, nr, kt);
+  __device__ long long total(const LatentAttnShape& sh, int nr, int kt, int lead) const {
+    return nb == 0 ? 0 : before(nb - 1, sh, nr, kt, lead) + lead + tiles(nb - 1, sh, nr, kt);
   }
 };
 
-// A CTA's stretch: where it starts and how many tiles it has.
+// A CTA's stretch: where it starts and how many places it has.
 struct LatentStart {
-  int n, b, tile;                   // sequence, block, first tile inside of the block
-  long long tiles;                  // tiles of the stretch (0: nothing to do)
-  long long pos;                    // its first tile in the line
-  long long W;                      // tiles of the line
+  int n, b, at;                     // sequence, block, first place inside of the block
+  long long places;                 // of the stretch (0: nothing to do)
+  long long pos;                    // its first place in the line
+  long long W;                      // places of the line
   int G;                            // CTAs that have a stretch
 };
 
 // All threads of the CTA (a multiple of 32, at most 1024); `sh_sum` 33 values.
 __device__ inline void latent_find_start(const LatentAttnShape& sh, const int32_t* seq_lens,
-                                         const int32_t* cu, int nr, int kt, LatentStart* st,
-                                         long long* sh_sum) {
+                                         const int32_t* cu, int nr, int kt, int lead,
+                                         LatentStart* st, long long* sh_sum) {
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
   const int per = (sh.N + nt - 1) / nt;
   const int n0 = min(tid * per, sh.N), n1 = min(n0 + per, sh.N);
   long long mine = 0;
-  for (int n = n0; n < n1; ++n) mine += LatentSeq(sh, seq_lens, cu, n, nr, kt).total(sh, nr, kt);
+  for (int n = n0; n < n1; ++n) mine += LatentSeq(sh, seq_lens, cu, n, nr, kt).total(sh, nr, kt, lead);
   long long run = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -174,9 +175,9 @@ __device__ inline void latent_find_start(const LatentAttnShape& sh, const int32_
     from = W * c / G;
     to = W * (c + 1) / G;
   }
-  long long at = sh_sum[warp] + run - mine;             // tiles before this thread's sequences
+  long long at = sh_sum[warp] + run - mine;             // places before this thread's sequences
   if (tid == 0) {
-    st->tiles = to - from;
+    st->places = to - from;
     st->pos = from;
     st->W = W;
     st->G = G;
@@ -184,17 +185,17 @@ __device__ inline void latent_find_start(const LatentAttnShape& sh, const int32_
   if (to > from && at <= from && from < at + mine) {
     for (int n = n0; n < n1; ++n) {
       const LatentSeq q(sh, seq_lens, cu, n, nr, kt);
-      const long long t = q.total(sh, nr, kt);
+      const long long t = q.total(sh, nr, kt, lead);
       if (from < at + t) {
         int lo = 0, hi = q.nb - 1;                       // the last block that starts at or before
         while (lo < hi) {
           const int mid = (lo + hi + 1) / 2;
-          if (at + q.before(mid, sh, nr, kt) <= from) lo = mid;
+          if (at + q.before(mid, sh, nr, kt, lead) <= from) lo = mid;
           else hi = mid - 1;
         }
         st->n = n;
         st->b = lo;
-        st->tile = (int)(from - at - q.before(lo, sh, nr, kt));
+        st->at = (int)(from - at - q.before(lo, sh, nr, kt, lead));
         break;
       }
       at += t;
@@ -210,40 +211,40 @@ struct LatentPiece {
   int len, start;                   // cached tokens; position of the sequence's first new token
   long long row0;                   // first row of the block in q (tokens * H + heads)
   int row_in_seq, rows;             // the same inside of the sequence; rows of the block
-  long long pos;                    // line position of tile t0
+  long long end;                    // the block's last place in the line
 };
 
 struct LatentWalk {
-  int n, b, tile;
+  int n, b, at;
   long long left, pos;
   __device__ explicit LatentWalk(const LatentStart& s)
-      : n(s.n), b(s.b), tile(s.tile), left(s.tiles), pos(s.pos) {}
+      : n(s.n), b(s.b), at(s.at), left(s.places), pos(s.pos) {}
   __device__ bool next(const LatentAttnShape& sh, const int32_t* seq_lens, const int32_t* cu,
-                       int nr, int kt, LatentPiece* p) {
-    if (left <= 0) return false;
-    while (n < sh.N) {
+                       int nr, int kt, int lead, LatentPiece* p) {
+    while (left > 0 && n < sh.N) {
       const LatentSeq q(sh, seq_lens, cu, n, nr, kt);
-      if (b < q.nb) {
-        p->n = n;
-        p->b = b;
-        p->tiles = q.cost(b, sh, nr, kt);
-        p->t0 = tile;
-        p->t1 = (int)min((long long)p->tiles, tile + left);
-        p->len = q.len;
-        p->start = q.len - q.cnt;
-        p->row_in_seq = b * nr;
-        p->rows = (int)min((long long)nr, (long long)q.cnt * sh.H - (long long)b * nr);
-        p->row0 = (long long)q.first * sh.H + (long long)b * nr;
-        p->pos = pos;
-        const int took = p->t1 - p->t0;
-        left -= took;
-        pos += took;
-        tile = 0;
-        ++b;
-        return true;
+      if (b >= q.nb) {
+        ++n;
+        b = 0;
+        continue;
       }
-      ++n;
-      b = 0;
+      p->n = n;
+      p->b = b;
+      p->tiles = q.tiles(b, sh, nr, kt);
+      const int took = (int)min((long long)(lead + p->tiles - at), left);
+      p->t0 = max(at - lead, 0);
+      p->t1 = at + took - lead;
+      p->len = q.len;
+      p->start = q.len - q.cnt;
+      p->row_in_seq = b * nr;
+      p->rows = (int)min((long long)nr, (long long)q.cnt * sh.H - (long long)b * nr);
+      p->row0 = (long long)q.first * sh.H + (long long)b * nr;
+      p->end = pos - at + lead + p->tiles - 1;
+      left -= took;
+      pos += took;
+      at = 0;
+      ++b;
+      if (p->t1 > 0) return true;                        // else the stretch ends in the empty places
     }
     return false;
   }

@@ -124,6 +124,7 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                      const int32_t* __restrict__ cu_seqlens, bf16* __restrict__ out,
                      float* __restrict__ lse, LatentAttnShape sh, TcPlan pl, LatentPartials pt) {
   constexpr int nr = NR, KT = tc_tile(NR), KK = KT / 16, kSBuf = NR <= 80 ? 2 : 1;
+  constexpr int kLead = NR <= 48 ? 2 : 3;           // tiles that a block costs besides its own
   constexpr uint32_t kTmemS = 4 * NR;
   // the alignment is part of the declaration: there is no room to round up
   extern __shared__ __align__(1024) uint8_t sm[];
@@ -164,7 +165,8 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
     fence_mbar_init();
     pt.head[blockIdx.x] = make_int4(0, 0, 0, 0);
   }
-  latent_find_start(sh, seq_lens, cu_seqlens, nr, KT, &st, reinterpret_cast<long long*>(s_red));
+  latent_find_start(sh, seq_lens, cu_seqlens, nr, KT, kLead, &st,
+                    reinterpret_cast<long long*>(s_red));
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -180,7 +182,7 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
     LatentWalk walk(st);
     LatentPiece p;
     uint32_t slot = 0, use = 0, turn = 0;
-    while (ok && walk.next(sh, seq_lens, cu_seqlens, nr, KT, &p)) {
+    while (ok && walk.next(sh, seq_lens, cu_seqlens, nr, KT, kLead, &p)) {
       // lane's group of tile t: its page (one past the cache, which reads as zeros, where there
       // is none)
       auto look = [&](int t) {
@@ -224,7 +226,7 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
     LatentWalk walk(st);
     LatentPiece p;
     uint32_t qi = 0, quse = 0;
-    while (ok && walk.next(sh, seq_lens, cu_seqlens, nr, KT, &p)) {
+    while (ok && walk.next(sh, seq_lens, cu_seqlens, nr, KT, kLead, &p)) {
       if (quse > 0) ok = __all_sync(kAll, mbar_wait(&bar.q_empty[qi], (quse - 1) & 1, kWaitLimit));
       if (!ok) break;
       if (elect_one()) {
@@ -285,7 +287,7 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
       return f;
     };
 
-    while (ok && walk.next(sh, seq_lens, cu_seqlens, nr, KT, &p)) {
+    while (ok && walk.next(sh, seq_lens, cu_seqlens, nr, KT, kLead, &p)) {
       const uint64_t q0 = dq + (uint64_t)(qi * (pl.q_bytes / 16));
       const int nt = p.t1 - p.t0;
       ok = __all_sync(kAll, mbar_wait(&bar.q_full[qi], quse & 1, kWaitLimit));
@@ -371,7 +373,7 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
       const uint32_t t = g - back;
       return mbar_wait(&bar.pv_done[pl.np == 2 ? t & 1 : 0], (pl.np == 2 ? t >> 1 : t) & 1, kWaitLimit);
     };
-    while (!dead && walk.next(sh, seq_lens, cu_seqlens, nr, KT, &p)) {
+    while (!dead && walk.next(sh, seq_lens, cu_seqlens, nr, KT, kLead, &p)) {
       const int low = p.start + p.row_in_seq / sh.H + 1; // the first row's limit, the least
       if (ts < nr) {                                     // rows behind the block: no weight at all
         s_m[ts] = ts < p.rows ? kNone : INFINITY;
@@ -554,7 +556,7 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
       }
       if (slot >= 0 && first && ts == 0)
         pt.head[blockIdx.x] =
-            make_int4((int)p.row0, p.rows, latent_cta_of(p.pos + p.tiles - 1, st.W, st.G), 0);
+            make_int4((int)p.row0, p.rows, latent_cta_of(p.end, st.W, st.G), 0);
       named_bar(1, kSoft);
       tc_fence_after();
       // 16 rows a load, the next one's under the stores: each stores 32 columns of a row a warp
