@@ -11,9 +11,10 @@
 // one under the arithmetic of this one, and each is used for both products by all 16 rows.
 // Scores: each of the eight warps takes an eighth of the columns of all 16 x 32, a thread
 // four rows by four tokens (eight 16-byte reads of shared memory for 64 FMAs); the eight
-// partial sums meet in shared memory.  Output: a thread holds eight rows by rank / 128
-// columns in registers (three reads for 8 rank / 128 FMAs).  Bound by the FMAs and these
-// reads, not by the cache's bytes: fp32 has no tensor-core form of fp32 accuracy.
+// partial sums meet in shared memory.  Output: a thread holds eight rows by four columns in
+// registers (three 16-byte reads for 32 FMAs); with a rank below 512 the threads that
+// remain take other tokens of the tile, and the sums meet at the end of a block.  Bound by
+// these reads, not by the cache's bytes: fp32 has no tensor-core form of fp32 accuracy.
 #include <type_traits>
 
 #include "latent_attn.cuh"
@@ -35,21 +36,6 @@ __device__ __forceinline__ float4 four(const __nv_bfloat16* x) {
   return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
                      __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
 }
-// kD neighbouring elements as fp32; the first one's index is a multiple of kD.
-template <int kD, typename T>
-__device__ __forceinline__ void load_few(const T* x, float (&v)[kD]) {
-  if constexpr (kD == 4) {
-    const float4 f = four(x);
-    v[0] = f.x;
-    v[1] = f.y;
-    v[2] = f.z;
-    v[3] = f.w;
-  } else {
-#pragma unroll
-    for (int i = 0; i < kD; ++i) v[i] = to_f32(x[i]);
-  }
-}
-
 // Shared memory: Q [16][LD], two tiles [32][LD] (LD = D + 16 bytes: rows shift by four banks),
 // the warps' partial scores.
 template <typename T> __host__ __device__ constexpr int simt_ld(int D) { return D + 16 / (int)sizeof(T); }
@@ -57,8 +43,9 @@ template <typename T> int simt_smem(int D) {
   return (kRows + 2 * kTile) * simt_ld<T>(D) * (int)sizeof(T) + 8 * kRows * kTile * 4;
 }
 
-// kD: value columns of a thread, rank / 128
-template <typename T, int kD>
+// kSplit: groups of threads that share a tile's tokens in the value product, at most
+// 512 / rank (384: one, which leaves two warps without columns).
+template <typename T, int kSplit>
 __global__ void __launch_bounds__(kNT)
 kda_latent_simt_kernel(const T* __restrict__ q, const T* __restrict__ cache,
                        const int32_t* __restrict__ page_table,
@@ -83,7 +70,9 @@ kda_latent_simt_kernel(const T* __restrict__ q, const T* __restrict__ cache,
   constexpr int E = 16 / sizeof(T);
   const int r = tid >> 4, j0 = tid & 15;                    // softmax: row r, tokens j0, j0 + 16
   const int rg = lane >> 3, tg = lane & 7, D8 = D / 8;      // scores: rows rg + 4 a, tokens tg + 8 b
-  const int hr = 8 * (tid & 1), d0 = (tid >> 1) * kD;       // output: rows hr .., columns d0 ..
+  // output: rows hr .., columns d0 .. of tokens [32 / kSplit * part, ..)
+  const int per = sh.rank / 2, part = tid / per, hr = 8 * (tid & 1), d0 = (tid - part * per) / 2 * 4;
+  const bool has = part < kSplit;
   LatentWalk walk(st);
   LatentPiece p;
   while (walk.next(sh, seq_lens, cu_seqlens, kRows, kTile, kLead, &p)) {
@@ -111,11 +100,11 @@ kda_latent_simt_kernel(const T* __restrict__ q, const T* __restrict__ cache,
         cp_async16(sq + row * LD + e, q + (p.row0 + from) * D + e, row < p.rows ? 16 : 0);
     }
     fetch(p.t0, 0);
-    float acc[8][kD];
+    float acc[8][4];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
-      for (int k = 0; k < kD; ++k) acc[i][k] = 0.f;
+      for (int k = 0; k < 4; ++k) acc[i][k] = 0.f;
     float m = -INFINITY, l = 0.f;
     const int lim = min(p.start + (p.row_in_seq + r) / sh.H + 1, p.len);
     const int low = p.start + p.row_in_seq / sh.H + 1;      // the block's first row's limit
@@ -182,26 +171,53 @@ kda_latent_simt_kernel(const T* __restrict__ q, const T* __restrict__ cache,
 #pragma unroll
       for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int k = 0; k < kD; ++k) acc[i][k] *= s_alpha[hr + i];
+        for (int k = 0; k < 4; ++k) acc[i][k] *= s_alpha[hr + i];
       const T* v0 = sk + b * kTile * LD + d0;
       auto add_values = [&](auto all) {                     // all: every row sees every token
+        constexpr int n = kTile / kSplit;
 #pragma unroll 4
-        for (int j = 0; j < kTile; ++j) {
-          float v[kD], w[8];
-          load_few<kD>(v0 + j * LD, v);
+        for (int j = n * part; j < n * (part + 1); ++j) {
+          float w[8];
+          const float4 v4 = four(v0 + j * LD);
+          const float v[4] = {v4.x, v4.y, v4.z, v4.w};
           *reinterpret_cast<float4*>(w) = *reinterpret_cast<const float4*>(&sp[j][hr]);
           *reinterpret_cast<float4*>(w + 4) = *reinterpret_cast<const float4*>(&sp[j][hr + 4]);
 #pragma unroll
           for (int i = 0; i < 8; ++i)
 #pragma unroll
-            for (int k = 0; k < kD; ++k)                    // a weight of zero takes nothing, not 0 * inf
+            for (int k = 0; k < 4; ++k)                     // a weight of zero takes nothing, not 0 * inf
               acc[i][k] = !decltype(all)::value && w[i] == 0.f ? acc[i][k]
                                                                : fmaf(w[i], v[k], acc[i][k]);
         }
       };
-      if (mixed) add_values(std::false_type());
-      else add_values(std::true_type());
+      if (has) {
+        if (mixed) add_values(std::false_type());
+        else add_values(std::true_type());
+      }
       __syncthreads();                                      // the tile and its weights are used
+    }
+    // ---- the token groups' sums, the upper half of the groups to the lower each time
+#pragma unroll
+    for (int h = kSplit / 2; h > 0; h /= 2) {               // h rank 16 floats: 16 KB at most
+      float* const x = sred + (part % h * 8 * per + tid % per) * 4;
+      if (part >= h && part < 2 * h) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<float4*>(x + i * per * 4) =
+              make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+      }
+      __syncthreads();
+      if (part < h) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float4 y = *reinterpret_cast<const float4*>(x + i * per * 4);
+          acc[i][0] += y.x;
+          acc[i][1] += y.y;
+          acc[i][2] += y.z;
+          acc[i][3] += y.w;
+        }
+      }
+      __syncthreads();
     }
     // ---- results: whole blocks to the output, shared ones to a partial slot
     const bool first = p.t0 == 0, last = p.t1 == p.tiles;
@@ -216,14 +232,20 @@ kda_latent_simt_kernel(const T* __restrict__ q, const T* __restrict__ cache,
       pt.head[blockIdx.x] =
           make_int4((int)p.row0, p.rows, latent_cta_of(p.end, st.W, st.G), 0);
     __syncthreads();
+    if (part == 0) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (hr + i >= p.rows) break;
+      for (int i = 0; i < 8; ++i) {
+        if (hr + i >= p.rows) break;
+        const float inv = s_inv[hr + i];
+        const float o[4] = {acc[i][0] * inv, acc[i][1] * inv, acc[i][2] * inv, acc[i][3] * inv};
+        if (slot >= 0) {
+          *reinterpret_cast<float4*>(pt.o + ((long long)slot * kRows + hr + i) * sh.rank + d0) =
+              make_float4(o[0], o[1], o[2], o[3]);
+        } else {
+          T* y = out + (p.row0 + hr + i) * sh.rank + d0;
 #pragma unroll
-      for (int k = 0; k < kD; ++k) {
-        const float o = acc[i][k] * s_inv[hr + i];
-        if (slot < 0) out[(p.row0 + hr + i) * sh.rank + d0 + k] = from_f32<T>(o);
-        else pt.o[((long long)slot * kRows + hr + i) * sh.rank + d0 + k] = o;
+          for (int k = 0; k < 4; ++k) y[k] = from_f32<T>(o[k]);
+        }
       }
     }
   }
@@ -402,10 +424,9 @@ using SimtKernel = void (*)(const T*, const T*, const int32_t*, const int32_t*, 
                             float*, LatentAttnShape, LatentPartials);
 template <typename T> SimtKernel<T> simt_kernel(int rank) {
   switch (rank) {
-    case 128: return kda_latent_simt_kernel<T, 1>;
+    case 128: return kda_latent_simt_kernel<T, 4>;
     case 256: return kda_latent_simt_kernel<T, 2>;
-    case 384: return kda_latent_simt_kernel<T, 3>;
-    default: return kda_latent_simt_kernel<T, 4>;
+    default: return kda_latent_simt_kernel<T, 1>;
   }
 }
 template <typename T> bool simt_setup() {
