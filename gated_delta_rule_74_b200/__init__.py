@@ -582,6 +582,15 @@ def _device_of(name: str, t: torch.Tensor) -> int:
     return t.get_device()
 
 
+def _new(stream, like: torch.Tensor, shape, dtype) -> torch.Tensor:
+    """An output that the call writes on `stream`: its memory comes from that stream's pool, as
+    memory of the current stream's may still be in use there."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
+
+
 def _take(name: str, t: Optional[torch.Tensor], dev: int, dtype, shape) -> Optional[int]:
     """Pointer of an optional contiguous tensor on device `dev`; one test for all of it, as a
     decode step's calls are as short as their checks."""
@@ -671,7 +680,7 @@ def kda_latent_append(kv: torch.Tensor, kv_cache: torch.Tensor, page_table: torc
     H, qp, qt, qh, op, ot, oh = 1, None, 0, 0, None, 0, 0
     if q_pe is not None:
         if q_pe_out is None:
-            q_pe_out = torch.empty(q_pe.shape, dtype=q_pe.dtype, device=q_pe.device)
+            q_pe_out = _new(stream, q_pe, q_pe.shape, q_pe.dtype)
         H = q_pe.shape[2] if q_pe.dim() == 4 else 0
         qp, qt, qh = _position_values("q_pe", q_pe, (B, T, H, rope), dtype, dev)
         op, ot, oh = _position_values("q_pe_out", q_pe_out, (B, T, H, rope), dtype, dev)
@@ -719,12 +728,12 @@ def kda_latent_attn(q: torch.Tensor, kv_cache: torch.Tensor, page_table: torch.T
     ptrs, nseq, sizes, dt = _latent_args(B, T, D, dtype, dev, kv_cache, page_table, seq_lens,
                                          cu_seqlens, rank)
     if out is None:
-        out = q.new_empty((B, T, H, rank))
+        out = _new(stream, q, (B, T, H, rank), dtype)
         op = out.data_ptr()
     else:
         op = _take("out", out, dev, dtype, (B, T, H, rank))
     if lse is None:
-        lse = torch.empty((B, T, H), dtype=torch.float32, device=q.device)
+        lse = _new(stream, q, (B, T, H), torch.float32)
         lp = lse.data_ptr()
     else:
         lp = _take("lse", lse, dev, torch.float32, (B, T, H))
@@ -756,12 +765,12 @@ def kda_verify_tokens(target: torch.Tensor, draft: Optional[torch.Tensor],
     dev = _device_of("target", target)
     xp = _take("draft_tokens", draft_tokens, dev, torch.int32, (N, L))
     if tokens is None:
-        tokens = draft_tokens.new_empty((N, L1))
+        tokens = _new(stream, draft_tokens, (N, L1), torch.int32)
         tp = tokens.data_ptr()
     else:
         tp = _take("tokens", tokens, dev, torch.int32, (N, L1))
     if accepted is None:
-        accepted = draft_tokens.new_empty((N,))
+        accepted = _new(stream, draft_tokens, (N,), torch.int32)
         ap = accepted.data_ptr()
     else:
         ap = _take("accepted", accepted, dev, torch.int32, (N,))

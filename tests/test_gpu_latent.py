@@ -239,6 +239,31 @@ def test_attn_workspace_and_stream(dtype):
         call(x, workspace=ws[:need - 256])
 
 
+def test_outputs_on_a_side_stream_are_that_streams():
+    """Work that the current stream still has queued on freed memory does not reach them."""
+    x = make("bf16", [300, 70], 2, 12, 512, 64, 64)
+    d = {k: (v.cuda() if isinstance(v, torch.Tensor) else v) for k, v in x.items()}
+    want = call(x)
+    target, u = torch.softmax(torch.randn((40, 5, 900), device="cuda"), -1), torch.rand((40, 5), device="cuda")
+    ids = target[:, :4].argmax(-1).to(torch.int32)
+    tok, acc = kda.kda_verify_tokens(target, None, ids, u)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    old = [torch.empty_like(t) for t in (*want, tok, acc)]
+    places = {t.data_ptr() for t in old}
+    torch.cuda._sleep(200_000_000)
+    for t in old:
+        t.fill_(7)
+    del old, t
+    got = (*kda.kda_latent_attn(d["q"], d["cache"], d["table"], d["lens"], rank=512, scale=x["scale"], stream=s),
+           *kda.kda_verify_tokens(target, None, ids, u, stream=s))
+    torch.cuda.synchronize()
+    for a, b in zip(got, (*want, tok, acc)):
+        assert torch.equal(a, b)
+        assert a.data_ptr() not in places
+
+
 def test_attn_two_streams_at_once():
     xs = [make("bf16", [3000, 100], 1, 12, 512, 64, 64, seed=s) for s in (1, 2)]
     want = [call(x) for x in xs]
