@@ -628,12 +628,18 @@ TcKernel tc_kernel(int nr) {
   }
 }
 
-// Rows of a block: all of a sequence's up to 96, a multiple of 16; of more, 64, whose tiles of
-// 64 tokens cost the MMAs less a row and token than 96 with tiles of 48 (a 1024-token chunk
-// of 12 heads behind 8192 to 32768 tokens: 562 us against 635).
+// Rows of a block: all of a sequence's up to 64, a multiple of 16.  Up to 96: all of them, or, of
+// few sequences, two blocks of 48: the CTAs then share a sequence by many, and what they
+// write and join counts for more than reading the cache twice (96 heads, 6000 tokens: 4
+// sequences 31 us against 41, 24 sequences 71 against 73, 43 of up to 16384 tokens 182 against
+// 152).  Of more rows, 64, whose tiles of 64 tokens cost the MMAs less a row and token than
+// 96 with tiles of 48 (a 1024-token chunk of 12 heads behind 8192 to 32768 tokens: 562 us
+// against 635).
 int tc_rows(int N, int L, int T, int H) {
   const long long rows = L > 0 ? (long long)L * H : (((long long)T + N - 1) / N) * H;
-  return rows <= kTcMaxRows ? (int)((rows + 15) / 16 * 16) : 64;
+  if (rows > kTcMaxRows) return 64;
+  if (rows > 64 && N <= 24) return 48;
+  return (int)((rows + 15) / 16 * 16);
 }
 
 }  // namespace

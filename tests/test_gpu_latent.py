@@ -112,13 +112,14 @@ def test_attn_rows_that_see_nothing(dtype, lens, L):
         assert bool((lse[n, :max(L - t, 0)] == -math.inf).all())
 
 
-@pytest.mark.parametrize("dtype,L,H", [("bf16", 6, 12), ("bf16", 3, 4), ("bf16", 4, 40), ("bf16", 3, 32),
-                                       ("f32", 6, 12)])
+@pytest.mark.parametrize("dtype,L,H,more", [("bf16", 6, 12, 0), ("bf16", 6, 12, 23), ("bf16", 3, 4, 0),
+                                            ("bf16", 4, 40, 0), ("bf16", 3, 32, 25), ("bf16", 4, 16, 0),
+                                            ("f32", 6, 12, 0)])
 @pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
-def test_attn_hidden_rows_have_no_effect(dtype, L, H, bad):
+def test_attn_hidden_rows_have_no_effect(dtype, L, H, more, bad):
     """NaN and infinities behind the length, in unused pages and in later new tokens."""
     page = 16
-    x = make(dtype, [70, 6, 33], L, H, 512, 64, page)
+    x = make(dtype, [70, 6, 33] + [9] * more, L, H, 512, 64, page)
     good = ref.attend(x["q"], x["cache"], x["table"], x["lens"], x["rank"], x["scale"])
     seen = torch.zeros(x["cache"].shape[:2], dtype=torch.bool)
     for n, t in enumerate(x["lens"].tolist()):
@@ -131,11 +132,11 @@ def test_attn_hidden_rows_have_no_effect(dtype, L, H, bad):
         close(y, out[n:n + 1, :L - 2], lse[n:n + 1, :L - 2], tuple(t[n:n + 1, :L - 2] for t in good))
 
 
-@pytest.mark.parametrize("dtype,H", [("bf16", 5), ("bf16", 12), ("bf16", 30), ("bf16", 48), ("bf16", 60),
-                                     ("f32", 12)])
-def test_attn_large_scores_and_far_maximum(dtype, H):
+@pytest.mark.parametrize("dtype,H,more", [("bf16", 5, 0), ("bf16", 12, 0), ("bf16", 30, 0), ("bf16", 48, 0), ("bf16", 60, 0),
+                                          ("bf16", 37, 23), ("bf16", 48, 23), ("f32", 12, 0)])
+def test_attn_large_scores_and_far_maximum(dtype, H, more):
     """Scores of hundreds, the largest one late: the running maximum has to move."""
-    x = make(dtype, [500, 257], 2, H, 256, 64, 64, spread=20.0)
+    x = make(dtype, [500, 257] + [3] * more, 2, H, 256, 64, 64, spread=20.0)
     pos = x["table"][0, 480 // 64], 480 % 64
     x["cache"][pos] = x["q"][0, 0, 0] / 4
     close(x, *call(x))
@@ -169,7 +170,8 @@ def test_attn_lengths_and_pages_out_of_range_stay_inside(dtype):
 
 
 @pytest.mark.parametrize("dtype,lens,H,rank,page", [
-    ("bf16", [9000], 12, 512, 64), ("bf16", [9500], 96, 512, 64), ("bf16", [5000, 40, 7000], 30, 384, 16),
+    ("bf16", [9000], 12, 512, 64), ("bf16", [9500], 96, 512, 64), ("bf16", [700] * 26, 96, 256, 64),
+    ("bf16", [5000, 40, 7000], 30, 384, 16),
     ("bf16", [900] * 9 + [1], 12, 128, 64), ("bf16", [9000, 100, 200, 300, 50, 60], 96, 256, 64),
     ("f32", [5000], 12, 256, 64), ("f32", [300] * 20, 3, 128, 64)])
 def test_attn_long_sequence_is_split_and_joined(dtype, lens, H, rank, page):
