@@ -4,11 +4,12 @@
 // A sequence's rows (new token i, head h -> row i H + h, contiguous in q) are cut into
 // blocks of `nr` rows; a block attends to the sequence's first `lim` tokens, lim the last
 // of its rows' causal limits, in tiles of `kt` tokens.  All tiles of all blocks form one
-// line, in order of sequence, block and tile, and CTA c of G takes the stretch
-// [W c / G, W (c + 1) / G) of its W tiles: every CTA the same number to within one,
+// line, in order of sequence, block and tile, each block's behind `lead` empty places for
+// what it costs besides (its start and its results), and CTA c of G takes the stretch
+// [W c / G, W (c + 1) / G) of its W places: every CTA the same number to within one,
 // whatever the lengths, with at most two blocks a CTA that others share.  A block that one
 // CTA has whole is written straight to `out`; of the others each CTA leaves a partial
-// result (normalised fp32 rows and their log-sums), which the combine kernel joins in the
+// result (normalised fp32 rows and their log-sums), which the join kernel adds up in the
 // order of the CTAs.  Nothing is planned on the host, which does not know the lengths.
 #pragma once
 
@@ -94,7 +95,7 @@ struct LatentSeq {
   int len, cnt, first;              // cached tokens, new tokens, first new token (row of q / H)
   int nb;                           // blocks
   int b1;                           // blocks before this one see no tile (one is counted)
-  long long base;                   // see cost()
+  long long base;                   // see tiles()
 
   __device__ LatentSeq(const LatentAttnShape& sh, const int32_t* seq_lens, const int32_t* cu,
                        int n, int nr, int kt) {
@@ -206,7 +207,7 @@ __device__ inline void latent_find_start(const LatentAttnShape& sh, const int32_
 
 // The pieces of a stretch, one after the other; every role of a CTA walks it for itself.
 struct LatentPiece {
-  int n, b;
+  int n;                            // sequence
   int t0, t1, tiles;                // tiles [t0, t1) of the block's `tiles`
   int len, start;                   // cached tokens; position of the sequence's first new token
   long long row0;                   // first row of the block in q (tokens * H + heads)
@@ -229,7 +230,6 @@ struct LatentWalk {
         continue;
       }
       p->n = n;
-      p->b = b;
       p->tiles = q.tiles(b, sh, nr, kt);
       const int took = (int)min((long long)(lead + p->tiles - at), left);
       p->t0 = max(at - lead, 0);

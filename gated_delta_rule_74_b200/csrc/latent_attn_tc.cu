@@ -1,6 +1,6 @@
 // Latent attention over a paged cache on the tensor cores (kda_latent_attn, bf16).
 //
-// For a block of up to 96 query rows (new token, head) and a tile of 64 cached rows C
+// For a block of up to 96 query rows (new token, head) and a tile of 64 or 48 cached rows C
 // [64][rank + rope], whose first `rank` columns are the values too:
 //     S^T (64 x rows)   = C Q^T                      tokens on the TMEM lanes
 //     P (64 x rows)     = 2^(scale log2e S - m)      to shared memory as bf16
@@ -25,7 +25,9 @@
 // The maximum that the weights refer to moves only when a score passes it by 2^8: a tile then
 // needs one vote, no reduction over the tokens, O^T is rescaled a few times a sequence, and
 // the weights stay below 2^8, far inside of bf16 and fp32.  Sums are kept by thread and
-// joined at the end of a block.
+// joined at the end of a block; O^T is added up in fp32 in TMEM (against 64 bits 0.0019 of the
+// output's norm, its own rounding and the weights', with 1M tokens a block, 0.004 with 4M, where
+// what the tensor core cuts off at each of 2^18 additions shows).
 // The scores of tile t + 1 go before the values of tile t when the tile is there before the
 // weights are.  The values' products run over 16 tokens at a time and hand those back to the
 // producers at once.  A wait between MMAs costs their warp 300 to 450 cycles, as long as eight
@@ -69,7 +71,6 @@ __host__ __device__ constexpr uint32_t tc_smem(int nr) { return nr > 80 ? 230400
 // Q, P.  A tile is groups of eight tokens, a group all of a row's 64-column chunks one after
 // the other, a chunk [8][128 B] with the 128-byte swizzle; a group comes by one TMA box.
 struct TcPlan {
-  int nr;                           // rows of a block, a multiple of 16 up to 96
   int npair, nch;                   // rank / 128; chunks of a row
   int ntile, nq, np;                // tiles of the ring; Q and P buffers
   uint32_t group, tile_bytes, q_bytes, p_bytes;
@@ -80,7 +81,6 @@ struct TcPlan {
 TcPlan tc_plan(int nr, int rank, int rope) {
   TcPlan p;
   const int kt = tc_tile(nr);
-  p.nr = nr;
   p.npair = rank / 128;
   p.nch = (rank + rope) / 64;
   p.group = (uint32_t)p.nch * 1024;

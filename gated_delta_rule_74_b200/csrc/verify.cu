@@ -8,7 +8,7 @@
 // (an fp32 product or difference is exact there, and the running sum is good to 1e-15).
 //
 // Bound by memory: of all the rows given, one target row and (after a rejection) one draft
-// row a sequence are read.  A cluster of C CTAs shares a sequence, each warp summing one
+// row a sequence are read.  A cluster of C CTAs shares a sequence, each warp summing
 // four neighbouring stretches of the vocabulary; the stretches' sums meet in the first CTA's
 // shared memory, whose first warp finds the stretch that the threshold falls into and reads
 // that one again, 256 elements at a time and the last of them lane by lane.  No atomics:

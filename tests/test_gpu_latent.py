@@ -132,8 +132,8 @@ def test_attn_hidden_rows_have_no_effect(dtype, L, H, more, bad):
         close(y, out[n:n + 1, :L - 2], lse[n:n + 1, :L - 2], tuple(t[n:n + 1, :L - 2] for t in good))
 
 
-@pytest.mark.parametrize("dtype,H,more", [("bf16", 5, 0), ("bf16", 12, 0), ("bf16", 30, 0), ("bf16", 48, 0), ("bf16", 60, 0),
-                                          ("bf16", 37, 23), ("bf16", 48, 23), ("f32", 12, 0)])
+@pytest.mark.parametrize("dtype,H,more", [("bf16", 5, 0), ("bf16", 12, 0), ("bf16", 30, 0), ("bf16", 48, 0),
+                                          ("bf16", 60, 0), ("bf16", 37, 23), ("bf16", 48, 23), ("f32", 12, 0)])
 def test_attn_large_scores_and_far_maximum(dtype, H, more):
     """Scores of hundreds, the largest one late: the running maximum has to move."""
     x = make(dtype, [500, 257] + [3] * more, 2, H, 256, 64, 64, spread=20.0)
