@@ -457,15 +457,18 @@ int simt_ctas(int sms) { return 2 * sms < kLatentMaxCtas ? 2 * sms : kLatentMaxC
 
 }  // namespace
 
-// `items`: blocks of rows of the call (packed: about).  Few of them are listed and spread over
-// the grid, two rounds at most of 2 us; a warp for each 128 columns of a row where some
-// CTAs share it; else blocks of 8 rows, of which many find nothing to do.
+// `items`: blocks of rows of the call (packed: about).  Few of them, each over more than 16
+// CTAs, are listed and spread over the grid, two rounds at most of 2 us (8 sequences of 16 heads,
+// rank 128: 15.7 us a call against 17.7); a warp for each 128 columns of a row where some
+// CTAs share it (16 sequences of 12 heads: 27.0 against 30.8 listed); else blocks of 8 rows, of
+// which many find nothing to do.
 cudaError_t launch_latent_join(void* out, float* lse, const LatentPartials& pt, int G, int nr,
                                int rank, long long items, int dtype, cudaStream_t stream) {
   const int units = nr * (rank / 128);
-  const bool list = items * units <= 8LL * G;
+  const bool list = items * units <= 8LL * G && items * 16 < G;
   const int y = items * kFew <= 2LL * G ? (units + 15) / 16 : nr <= 32 ? 4 : (nr + 7) / 8;
-  const dim3 grid = list ? dim3(4 * G) : dim3(G, y);
+  const long long most = 4LL * G, work = items * units;
+  const dim3 grid = list ? dim3((unsigned)(work < most ? work : most)) : dim3(G, y);
   cudaError_t e = cudaSuccess;
   if (dtype == KDA_BF16)
     KDA_TIMED(KDA_KERNEL_LATENT_ATTN, stream,
