@@ -352,7 +352,8 @@ int latent_attn_impl(const void* q, const void* kv_cache, const int32_t* page_ta
   if (ws) {
     int sms = 0;
     if (!current_sms(&sms)) return KDA_ERR_CUDA;
-    if (!workspace_ok(ws, kda::latent_attn_scratch_bytes(N, sh.L, L, H, rank, page_size, dtype, sms)))
+    if (!workspace_ok(ws, kda::latent_attn_scratch_bytes(N, sh.L, L, H, rank, rope, page_size,
+                                                         dtype, sms)))
       return KDA_ERR_INVALID_ARG;
   }
   if (L == 0) return KDA_OK;                        // no new tokens: nothing to write
@@ -441,7 +442,7 @@ int kda_latent_attn_workspace_size(int N, int L, int H, int rank, int rope, int 
                                  dtype, packed != 0);
   if (rc != KDA_OK) return rc;
   if (sms == 0 && !current_sms(&sms)) return KDA_ERR_CUDA;
-  *bytes = kda::latent_attn_scratch_bytes(N, packed ? 0 : L, L, H, rank, page_size, dtype, sms);
+  *bytes = kda::latent_attn_scratch_bytes(N, packed ? 0 : L, L, H, rank, rope, page_size, dtype, sms);
   return KDA_OK;
 }
 

@@ -453,7 +453,13 @@ cudaError_t run_simt(const void* q, const void* cache, const int32_t* page_table
                             sizeof(T) == 2 ? KDA_BF16 : KDA_F32, stream);
 }
 
-int simt_ctas(int sms) { return 2 * sms < kLatentMaxCtas ? 2 * sms : kLatentMaxCtas; }
+// CTAs that are resident at once: two an SM where their shared memory fits (4 KB: the variables and
+// what the system keeps), else one; more would go in two rounds, each with its start and results.
+int simt_ctas(int sms, int D, int dtype) {
+  const int smem = dtype == KDA_BF16 ? simt_smem<__nv_bfloat16>(D) : simt_smem<float>(D);
+  const int n = 2 * (smem + 4096) <= 228 * 1024 ? 2 * sms : sms;
+  return n < kLatentMaxCtas ? n : kLatentMaxCtas;
+}
 
 }  // namespace
 
@@ -487,11 +493,11 @@ long long latent_items(const LatentAttnShape& sh, int nr) {
                   : ((long long)sh.T * sh.H + nr - 1) / nr;
 }
 
-size_t latent_attn_scratch_bytes(int N, int L, int T, int H, int rank, int page_size, int dtype,
-                                 int sms) {
+size_t latent_attn_scratch_bytes(int N, int L, int T, int H, int rank, int rope, int page_size,
+                                 int dtype, int sms) {
   if (latent_tc_supported(dtype, page_size))
     return latent_tc_scratch_bytes(N, L, T, H, rank, sms);
-  return latent_scratch_bytes(simt_ctas(sms), kRows, rank);
+  return latent_scratch_bytes(simt_ctas(sms, rank + rope, dtype), kRows, rank);
 }
 
 cudaError_t launch_latent_attn(const void* q, const void* cache, const int32_t* page_table,
@@ -505,7 +511,8 @@ cudaError_t launch_latent_attn(const void* q, const void* cache, const int32_t* 
                        []() { return simt_setup<float>() && simt_setup<__nv_bfloat16>(); }))
     return cudaErrorInvalidDevice;
   const size_t bytes =
-      latent_attn_scratch_bytes(sh.N, sh.L, sh.T, sh.H, sh.rank, sh.page_size, dtype, sms);
+      latent_attn_scratch_bytes(sh.N, sh.L, sh.T, sh.H, sh.rank, sh.rope, sh.page_size, dtype,
+                                sms);
   void* buf = ws ? ws->ptr : nullptr;
   cudaError_t e;
   if (!ws) {
@@ -513,7 +520,7 @@ cudaError_t launch_latent_attn(const void* q, const void* cache, const int32_t* 
     e = cudaMallocFromPoolAsync(&buf, bytes, pool, stream);
     if (e != cudaSuccess) return e;
   }
-  const int G = simt_ctas(sms);
+  const int G = simt_ctas(sms, sh.rank + sh.rope, dtype);
   const LatentPartials pt = latent_partials(buf, G, kRows);
   if (latent_tc_supported(dtype, sh.page_size))
     e = launch_latent_tc(q, cache, page_table, seq_lens, cu_seqlens, out, lse, sh, sms, buf, stream);

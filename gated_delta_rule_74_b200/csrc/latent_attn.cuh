@@ -47,8 +47,8 @@ inline LatentPartials latent_partials(void* ws, int G, int nr) {
 }
 
 // Scratch bytes of one call; rows a sequence has (packed: on average) decide the block.
-size_t latent_attn_scratch_bytes(int N, int L, int T, int H, int rank, int page_size, int dtype,
-                                 int sms);
+size_t latent_attn_scratch_bytes(int N, int L, int T, int H, int rank, int rope, int page_size,
+                                 int dtype, int sms);
 cudaError_t launch_latent_attn(const void* q, const void* cache, const int32_t* page_table,
                                const int32_t* seq_lens, const int32_t* cu_seqlens, void* out,
                                float* lse, const LatentAttnShape& sh, int dtype,
