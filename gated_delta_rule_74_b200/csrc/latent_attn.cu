@@ -454,7 +454,10 @@ cudaError_t run_simt(const void* q, const void* cache, const int32_t* page_table
 }
 
 // CTAs that are resident at once: two an SM where their shared memory fits (4 KB: the variables and
-// what the system keeps), else one; more would go in two rounds, each with its start and results.
+// what the system keeps), else one; more would go in two rounds, each with its start and results
+// (fp32, rank 512, 12 heads, up to 4000 tokens: 4 sequences 28.5 us against 38.2, 8 44.2 against
+// 54.5).  One CTA of 512 threads instead is slower (32 sequences of up to
+// 8000 tokens 259 us against 250): what bounds it is shared memory, not the warps there are.
 int simt_ctas(int sms, int D, int dtype) {
   const int smem = dtype == KDA_BF16 ? simt_smem<__nv_bfloat16>(D) : simt_smem<float>(D);
   const int n = 2 * (smem + 4096) <= 228 * 1024 ? 2 * sms : sms;
