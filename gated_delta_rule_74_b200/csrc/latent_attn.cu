@@ -15,6 +15,9 @@
 // registers (three 16-byte reads for 32 FMAs); with a rank below 512 the threads that
 // remain take other tokens of the tile, and the sums meet at the end of a block.  Bound by
 // these reads, not by the cache's bytes: fp32 has no tensor-core form of fp32 accuracy.
+// Where there are more rows and shared memory holds but one such CTA an SM, a CTA holds 32 rows
+// and tiles of 16 tokens instead: half a warp a sixteenth of the columns, eight rows by four
+// tokens a thread (12 reads for 128 FMAs), 16 rows by four columns of the output (five for 64).
 #include <type_traits>
 
 #include "latent_attn.cuh"
@@ -24,8 +27,6 @@ namespace kda {
 namespace {
 
 constexpr int kNT = 256;
-constexpr int kRows = 16;                // rows of a block
-constexpr int kTile = 32;                // cached rows of a tile
 constexpr int kLead = 1;                 // tiles that a block costs besides its own
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -39,26 +40,36 @@ __device__ __forceinline__ float4 four(const __nv_bfloat16* x) {
 // Shared memory: Q [16][LD], two tiles [32][LD] (LD = D + 16 bytes: rows shift by four banks),
 // the warps' partial scores.
 template <typename T> __host__ __device__ constexpr int simt_ld(int D) { return D + 16 / (int)sizeof(T); }
-template <typename T> int simt_smem(int D) {
-  return (kRows + 2 * kTile) * simt_ld<T>(D) * (int)sizeof(T) + 8 * kRows * kTile * 4;
+// Cached rows of a tile, and floats of a warp's partial scores' row (32 rows: padded for the banks).
+__host__ __device__ constexpr int simt_tile(int rows) { return 512 / rows; }
+__host__ __device__ constexpr int simt_red_ld(int rows) { return rows == 16 ? 32 : 20; }
+// Floats of the partial scores, in whose place the token groups' sums meet in the end.
+__host__ __device__ constexpr int simt_red(int rows, int split) {
+  return rows == 16 ? 4096 : split > 1 ? 8192 : 8 * 32 * simt_red_ld(32);
+}
+int simt_split(int rank) { return rank == 128 ? 4 : rank == 256 ? 2 : 1; }
+template <typename T> int simt_smem(int D, int rank, int rows) {
+  return (rows + 2 * simt_tile(rows)) * simt_ld<T>(D) * (int)sizeof(T) +
+         simt_red(rows, simt_split(rank)) * 4;
 }
 
 // kSplit: groups of threads that share a tile's tokens in the value product, at most
 // 512 / rank (384: one, which leaves two warps without columns).
-template <typename T, int kSplit>
-__global__ void __launch_bounds__(kNT)
+template <typename T, int kRows, int kSplit>
+__global__ void __launch_bounds__(kNT, kRows == 16 ? 2 : 1)
 kda_latent_simt_kernel(const T* __restrict__ q, const T* __restrict__ cache,
                        const int32_t* __restrict__ page_table,
                        const int32_t* __restrict__ seq_lens,
                        const int32_t* __restrict__ cu_seqlens, T* __restrict__ out,
                        float* __restrict__ lse, LatentAttnShape sh, LatentPartials pt) {
   using namespace sm100;
+  constexpr int kTile = simt_tile(kRows), kRL = simt_red_ld(kRows);
   extern __shared__ float4 smem4[];
   const int D = sh.rank + sh.rope, LD = simt_ld<T>(D);
   T* const sq = reinterpret_cast<T*>(smem4);
   T* const sk = sq + kRows * LD;
-  float* const sred = reinterpret_cast<float*>(sk + 2 * kTile * LD);   // [8][16][32]
-  __shared__ __align__(16) float sp[kTile][kRows];
+  float* const sred = reinterpret_cast<float*>(sk + 2 * kTile * LD);   // [8][kRows][kRL]
+  __shared__ __align__(16) float sp[kTile][kRows + 4];
   __shared__ __align__(16) float s_alpha[kRows];
   __shared__ float s_inv[kRows];
   __shared__ LatentStart st;
@@ -68,17 +79,22 @@ kda_latent_simt_kernel(const T* __restrict__ q, const T* __restrict__ cache,
   if (tid == 0) pt.head[blockIdx.x] = make_int4(0, 0, 0, 0);
 
   constexpr int E = 16 / sizeof(T);
-  const int r = tid >> 4, j0 = tid & 15;                    // softmax: row r, tokens j0, j0 + 16
-  const int rg = lane >> 3, tg = lane & 7, D8 = D / 8;      // scores: rows rg + 4 a, tokens tg + 8 b
-  // output: rows hr .., columns d0 .. of tokens [32 / kSplit * part, ..)
-  const int per = sh.rank / 2, part = tid / per, hr = 8 * (tid & 1), d0 = (tid - part * per) / 2 * 4;
+  constexpr int kRT = kNT / kRows, kTG = kTile / 4;         // threads of a row; groups of tokens
+  const int r = tid / kRT, j0 = tid % kRT;                  // softmax: row r, tokens j0, j0 + kRT
+  // scores: rows rg + 4 a, tokens tg + kTG b of 4 kTG lanes; those share an equal part of the columns
+  constexpr int kA = kRows / 4, kSl = kNT / (4 * kTG);
+  const int rg = lane / kTG % 4, tg = lane % kTG, sl = tid / (4 * kTG), DS = D / kSl;
+  // output: rows hr .., columns d0 .. of tokens [kTile / kSplit * part, ..)
+  constexpr int kH = kRows / 2;
+  const int per = sh.rank / 2, part = tid / per, hr = kH * (tid & 1), d0 = (tid - part * per) / 2 * 4;
   const bool has = part < kSplit;
   LatentWalk walk(st);
   LatentPiece p;
   while (walk.next(sh, seq_lens, cu_seqlens, kRows, kTile, kLead, &p)) {
-    // tile t into buffer b, eight threads a row; zeros where there is no row
+    // tile t into buffer b; zeros where there is no row
     auto fetch = [&](int t, int b) {
-      const int row = tid >> 3, pos = t * kTile + row;
+      constexpr int kT = kNT / kTile;                       // threads of a row
+      const int row = tid / kT, pos = t * kTile + row;
       const T* src = cache;
       uint32_t bytes = 0;
       if (pos < p.len) {
@@ -89,20 +105,20 @@ kda_latent_simt_kernel(const T* __restrict__ q, const T* __restrict__ cache,
           bytes = 16;
         }
       }
-      for (int e = (tid & 7) * E; e < D; e += 8 * E)
+      for (int e = tid % kT * E; e < D; e += kT * E)
         cp_async16(sk + (b * kTile + row) * LD + e, src + (bytes ? e : 0), bytes);
       cp_async_commit();
     };
     __syncthreads();                                        // the block before is done with
     {
-      const int row = tid >> 4, from = row < p.rows ? row : 0;
-      for (int e = (tid & 15) * E; e < D; e += 16 * E)
-        cp_async16(sq + row * LD + e, q + (p.row0 + from) * D + e, row < p.rows ? 16 : 0);
+      const int from = r < p.rows ? r : 0;
+      for (int e = j0 * E; e < D; e += kRT * E)
+        cp_async16(sq + r * LD + e, q + (p.row0 + from) * D + e, r < p.rows ? 16 : 0);
     }
     fetch(p.t0, 0);
-    float acc[8][4];
+    float acc[kH][4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < kH; ++i)
 #pragma unroll
       for (int k = 0; k < 4; ++k) acc[i][k] = 0.f;
     float m = -INFINITY, l = 0.f;
@@ -118,58 +134,65 @@ kda_latent_simt_kernel(const T* __restrict__ q, const T* __restrict__ cache,
       }
       __syncthreads();                                      // this tile is there
       {
-        float x[4][4] = {};
-        const T* a = sq + rg * LD + warp * D8;
-        const T* y = sk + (b * kTile + tg) * LD + warp * D8;
+        float x[kA][4] = {};
+        const T* a = sq + rg * LD + sl * DS;
+        const T* y = sk + (b * kTile + tg) * LD + sl * DS;
 #pragma unroll 2
-        for (int d = 0; d < D8; d += 4) {
-          float4 av[4], yv[4];
+        for (int d = 0; d < DS; d += 4) {
+          float4 av[kA], yv[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            av[i] = four(a + 4 * i * LD + d);
-            yv[i] = four(y + 8 * i * LD + d);
-          }
+          for (int i = 0; i < kA; ++i) av[i] = four(a + 4 * i * LD + d);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int j = 0; j < 4; ++j) yv[j] = four(y + kTG * j * LD + d);
+#pragma unroll
+          for (int i = 0; i < kA; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
               x[i][j] = fmaf(av[i].x, yv[j].x, fmaf(av[i].y, yv[j].y,
                         fmaf(av[i].z, yv[j].z, fmaf(av[i].w, yv[j].w, x[i][j]))));
         }
+        // of 32 rows a warp has two parts of the columns: each half keeps half of the rows
+        const bool up = kA == 8 && lane >= 16;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            sred[(warp * kRows + rg + 4 * i) * kTile + tg + 8 * j] = x[i][j];
+          for (int j = 0; j < 4; ++j) {
+            float v = x[i][j];
+            if constexpr (kA == 8) {
+              const float w = x[i + 4][j], give = up ? v : w;
+              v = (up ? w : v) + __shfl_xor_sync(0xffffffffu, give, 16);
+            }
+            sred[(warp * kRows + rg + 4 * i + (up ? 16 : 0)) * kRL + tg + kTG * j] = v;
+          }
       }
       __syncthreads();
       float s0 = 0.f, s1 = 0.f;
 #pragma unroll
       for (int w = 0; w < 8; ++w) {
-        s0 += sred[(w * kRows + r) * kTile + j0];
-        s1 += sred[(w * kRows + r) * kTile + j0 + 16];
+        s0 += sred[(w * kRows + r) * kRL + j0];
+        s1 += sred[(w * kRows + r) * kRL + j0 + kRT];
       }
       const float c = sh.scale * kLog2e;
       s0 = k0 + j0 < lim ? s0 * c : -INFINITY;
-      s1 = k0 + j0 + 16 < lim ? s1 * c : -INFINITY;
+      s1 = k0 + j0 + kRT < lim ? s1 * c : -INFINITY;
       float mx = fmaxf(s0, s1);
 #pragma unroll
-      for (int o = 8; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o, 16));
+      for (int o = kRT / 2; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
       const float mn = fmaxf(m, mx), ms = mn == -INFINITY ? 0.f : mn;
       const float p0 = exp2f(s0 - ms), p1 = exp2f(s1 - ms);   // a NaN score gives a NaN weight
       float ls = p0 + p1;
 #pragma unroll
-      for (int o = 8; o; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o, 16);
+      for (int o = kRT / 2; o; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
       const float al = exp2f(m - ms);
       l = l * al + ls;
       m = mn;
       sp[j0][r] = p0;
-      sp[j0 + 16][r] = p1;
+      sp[j0 + kRT][r] = p1;
       if (j0 == 0) s_alpha[r] = al;
       __syncthreads();
       const bool mixed = k0 + kTile > low;                  // some row does not see some token
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int i = 0; i < kH; ++i)
 #pragma unroll
         for (int k = 0; k < 4; ++k) acc[i][k] *= s_alpha[hr + i];
       const T* v0 = sk + b * kTile * LD + d0;
@@ -177,13 +200,14 @@ kda_latent_simt_kernel(const T* __restrict__ q, const T* __restrict__ cache,
         constexpr int n = kTile / kSplit;
 #pragma unroll 4
         for (int j = n * part; j < n * (part + 1); ++j) {
-          float w[8];
+          float w[kH];
           const float4 v4 = four(v0 + j * LD);
           const float v[4] = {v4.x, v4.y, v4.z, v4.w};
-          *reinterpret_cast<float4*>(w) = *reinterpret_cast<const float4*>(&sp[j][hr]);
-          *reinterpret_cast<float4*>(w + 4) = *reinterpret_cast<const float4*>(&sp[j][hr + 4]);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
+          for (int i = 0; i < kH; i += 4)
+            *reinterpret_cast<float4*>(w + i) = *reinterpret_cast<const float4*>(&sp[j][hr + i]);
+#pragma unroll
+          for (int i = 0; i < kH; ++i)
 #pragma unroll
             for (int k = 0; k < 4; ++k)                     // a weight of zero takes nothing, not 0 * inf
               acc[i][k] = !decltype(all)::value && w[i] == 0.f ? acc[i][k]
@@ -198,18 +222,18 @@ kda_latent_simt_kernel(const T* __restrict__ q, const T* __restrict__ cache,
     }
     // ---- the token groups' sums, the upper half of the groups to the lower each time
 #pragma unroll
-    for (int h = kSplit / 2; h > 0; h /= 2) {               // h rank 16 floats: 16 KB at most
-      float* const x = sred + (part % h * 8 * per + tid % per) * 4;
+    for (int h = kSplit / 2; h > 0; h /= 2) {               // h rank kRows floats: all of sred at most
+      float* const x = sred + (part % h * kH * per + tid % per) * 4;
       if (part >= h && part < 2 * h) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < kH; ++i)
           *reinterpret_cast<float4*>(x + i * per * 4) =
               make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
       }
       __syncthreads();
       if (part < h) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < kH; ++i) {
           const float4 y = *reinterpret_cast<const float4*>(x + i * per * 4);
           acc[i][0] += y.x;
           acc[i][1] += y.y;
@@ -234,7 +258,7 @@ kda_latent_simt_kernel(const T* __restrict__ q, const T* __restrict__ cache,
     __syncthreads();
     if (part == 0) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < kH; ++i) {
         if (hr + i >= p.rows) break;
         const float inv = s_inv[hr + i];
         const float o[4] = {acc[i][0] * inv, acc[i][1] * inv, acc[i][2] * inv, acc[i][3] * inv};
@@ -422,46 +446,65 @@ kda_latent_join_kernel(T* __restrict__ out, float* __restrict__ lse, LatentParti
 template <typename T>
 using SimtKernel = void (*)(const T*, const T*, const int32_t*, const int32_t*, const int32_t*, T*,
                             float*, LatentAttnShape, LatentPartials);
-template <typename T> SimtKernel<T> simt_kernel(int rank) {
-  switch (rank) {
-    case 128: return kda_latent_simt_kernel<T, 4>;
-    case 256: return kda_latent_simt_kernel<T, 2>;
-    default: return kda_latent_simt_kernel<T, 1>;
+template <typename T> SimtKernel<T> simt_kernel(int rank, int rows) {
+  if constexpr (sizeof(T) == 4)
+    if (rows == 32)
+      return rank == 256 ? kda_latent_simt_kernel<T, 32, 2> : kda_latent_simt_kernel<T, 32, 1>;
+  switch (simt_split(rank)) {
+    case 4: return kda_latent_simt_kernel<T, 16, 4>;
+    case 2: return kda_latent_simt_kernel<T, 16, 2>;
+    default: return kda_latent_simt_kernel<T, 16, 1>;
   }
 }
 template <typename T> bool simt_setup() {
   for (int rank = 128; rank <= 512; rank += 128)
-    if (cudaFuncSetAttribute(simt_kernel<T>(rank), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             simt_smem<T>(rank + 64)) != cudaSuccess)
-      return false;
+    for (int rows = 16; rows <= 32; rows += 16)
+      if (cudaFuncSetAttribute(simt_kernel<T>(rank, rows), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               simt_smem<T>(512 + 64, 512, 16)) != cudaSuccess)
+        return false;
   return true;
+}
+
+// Whether two CTAs of 16 rows fit an SM (4 KB: the variables and what the system keeps).
+bool simt_two(int D, int rank, int dtype) {
+  const int smem =
+      dtype == KDA_BF16 ? simt_smem<__nv_bfloat16>(D, rank, 16) : simt_smem<float>(D, rank, 16);
+  return 2 * (smem + 4096) <= 228 * 1024;
+}
+
+// Rows of a block: 32 where two CTAs of 16 do not fit an SM (fp32 from 320 columns on) and few of
+// the rows would be empty (2 x 200 tokens of 12 heads behind 3000, rank 512: 655 us against 814;
+// rank 256 122 against 126).  Where two fit they are faster (4 x 16 tokens of 96 heads, bf16,
+// 1315 against 1364; rank 128 141 against 148).  Packed: of a sequence's rows on average.
+int simt_rows(int N, int L, int T, int H, int D, int rank, int dtype) {
+  const long long rows = L > 0 ? (long long)L * H : (((long long)T + N - 1) / N) * H;
+  return !simt_two(D, rank, dtype) && (rows > 96 || (rows + 15) / 16 % 2 == 0) ? 32 : 16;
+}
+
+// CTAs that are resident at once: more would go in two rounds, each with its start and results
+// (fp32, rank 512, 12 heads, up to 4000 tokens: 4 sequences 28.5 us against 38.2, 8 44.2 against
+// 54.5).  One CTA of 512 threads where two of 256 do not fit is slower (32 sequences of up to 8000
+// tokens 259 us against 250): what bounds it is shared memory, not the warps there are.
+int simt_ctas(int sms, int D, int rank, int dtype) {
+  const int n = simt_two(D, rank, dtype) ? 2 * sms : sms;
+  return n < kLatentMaxCtas ? n : kLatentMaxCtas;
 }
 
 template <typename T>
 cudaError_t run_simt(const void* q, const void* cache, const int32_t* page_table,
                      const int32_t* seq_lens, const int32_t* cu, void* out, float* lse,
-                     const LatentAttnShape& sh, int G, const LatentPartials& pt,
+                     const LatentAttnShape& sh, int rows, int G, const LatentPartials& pt,
                      cudaStream_t stream) {
+  const int smem = simt_smem<T>(sh.rank + sh.rope, sh.rank, rows);
   KDA_TIMED(KDA_KERNEL_LATENT_ATTN, stream,
-            simt_kernel<T>(sh.rank)<<<G, kNT, simt_smem<T>(sh.rank + sh.rope), stream>>>(
+            simt_kernel<T>(sh.rank, rows)<<<G, kNT, smem, stream>>>(
                 static_cast<const T*>(q), static_cast<const T*>(cache), page_table, seq_lens, cu,
                 static_cast<T*>(out), lse, sh, pt));
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   note_launches(1);
-  return launch_latent_join(out, lse, pt, G, kRows, sh.rank, latent_items(sh, kRows),
+  return launch_latent_join(out, lse, pt, G, rows, sh.rank, latent_items(sh, rows),
                             sizeof(T) == 2 ? KDA_BF16 : KDA_F32, stream);
-}
-
-// CTAs that are resident at once: two an SM where their shared memory fits (4 KB: the variables and
-// what the system keeps), else one; more would go in two rounds, each with its start and results
-// (fp32, rank 512, 12 heads, up to 4000 tokens: 4 sequences 28.5 us against 38.2, 8 44.2 against
-// 54.5).  One CTA of 512 threads instead is slower (32 sequences of up to
-// 8000 tokens 259 us against 250): what bounds it is shared memory, not the warps there are.
-int simt_ctas(int sms, int D, int dtype) {
-  const int smem = dtype == KDA_BF16 ? simt_smem<__nv_bfloat16>(D) : simt_smem<float>(D);
-  const int n = 2 * (smem + 4096) <= 228 * 1024 ? 2 * sms : sms;
-  return n < kLatentMaxCtas ? n : kLatentMaxCtas;
 }
 
 }  // namespace
@@ -500,7 +543,8 @@ size_t latent_attn_scratch_bytes(int N, int L, int T, int H, int rank, int rope,
                                  int dtype, int sms) {
   if (latent_tc_supported(dtype, page_size))
     return latent_tc_scratch_bytes(N, L, T, H, rank, sms);
-  return latent_scratch_bytes(simt_ctas(sms, rank + rope, dtype), kRows, rank);
+  return latent_scratch_bytes(simt_ctas(sms, rank + rope, rank, dtype),
+                              simt_rows(N, L, T, H, rank + rope, rank, dtype), rank);
 }
 
 cudaError_t launch_latent_attn(const void* q, const void* cache, const int32_t* page_table,
@@ -523,15 +567,16 @@ cudaError_t launch_latent_attn(const void* q, const void* cache, const int32_t* 
     e = cudaMallocFromPoolAsync(&buf, bytes, pool, stream);
     if (e != cudaSuccess) return e;
   }
-  const int G = simt_ctas(sms, sh.rank + sh.rope, dtype);
-  const LatentPartials pt = latent_partials(buf, G, kRows);
+  const int D = sh.rank + sh.rope, rows = simt_rows(sh.N, sh.L, sh.T, sh.H, D, sh.rank, dtype);
+  const int G = simt_ctas(sms, D, sh.rank, dtype);
+  const LatentPartials pt = latent_partials(buf, G, rows);
   if (latent_tc_supported(dtype, sh.page_size))
     e = launch_latent_tc(q, cache, page_table, seq_lens, cu_seqlens, out, lse, sh, sms, buf, stream);
   else
     e = dtype == KDA_BF16 ? run_simt<__nv_bfloat16>(q, cache, page_table, seq_lens, cu_seqlens, out,
-                                                  lse, sh, G, pt, stream)
+                                                  lse, sh, rows, G, pt, stream)
                         : run_simt<float>(q, cache, page_table, seq_lens, cu_seqlens, out, lse, sh,
-                                          G, pt, stream);
+                                          rows, G, pt, stream);
   if (!ws) {
     const cudaError_t f = cudaFreeAsync(buf, stream);
     if (e == cudaSuccess) e = f;

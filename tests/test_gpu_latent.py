@@ -78,7 +78,9 @@ CASES = [
     ("bf16", [33, 64], 1, 16, 512, 64, 1), ("bf16", [200], 37, 7, 256, 64, 256),
     ("f32", [1], 1, 1, 512, 64, 64), ("f32", [64, 65, 31, 0, 1, 300], 1, 12, 256, 0, 32),
     ("f32", [5, 130], 4, 12, 512, 64, 48), ("f32", [90, 33], 3, 40, 384, 64, 7),
-    ("f32", [77, 20], 21, 3, 128, 64, 16),
+    ("f32", [77, 20], 21, 3, 128, 64, 16), ("f32", [70, 0, 33], 5, 32, 512, 64, 48),
+    ("f32", [200, 16], 2, 16, 256, 64, 5), ("f32", [15, 16, 17, 1], 1, 30, 512, 0, 16),
+    ("f32", [129], 37, 7, 384, 0, 64),
 ]
 
 
@@ -114,7 +116,7 @@ def test_attn_rows_that_see_nothing(dtype, lens, L):
 
 @pytest.mark.parametrize("dtype,L,H,more", [("bf16", 6, 12, 0), ("bf16", 6, 12, 23), ("bf16", 3, 4, 0),
                                             ("bf16", 4, 40, 0), ("bf16", 3, 32, 25), ("bf16", 4, 16, 0),
-                                            ("f32", 6, 12, 0)])
+                                            ("f32", 6, 12, 0), ("f32", 6, 32, 0)])
 @pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
 def test_attn_hidden_rows_have_no_effect(dtype, L, H, more, bad):
     """NaN and infinities behind the length, in unused pages and in later new tokens."""
@@ -133,7 +135,8 @@ def test_attn_hidden_rows_have_no_effect(dtype, L, H, more, bad):
 
 
 @pytest.mark.parametrize("dtype,H,more", [("bf16", 5, 0), ("bf16", 12, 0), ("bf16", 30, 0), ("bf16", 48, 0),
-                                          ("bf16", 60, 0), ("bf16", 37, 23), ("bf16", 48, 23), ("f32", 12, 0)])
+                                          ("bf16", 60, 0), ("bf16", 37, 23), ("bf16", 48, 23), ("f32", 12, 0),
+                                          ("f32", 16, 0)])
 def test_attn_large_scores_and_far_maximum(dtype, H, more):
     """Scores of hundreds, the largest one late: the running maximum has to move."""
     x = make(dtype, [500, 257] + [3] * more, 2, H, 256, 64, 64, spread=20.0)
@@ -173,7 +176,8 @@ def test_attn_lengths_and_pages_out_of_range_stay_inside(dtype):
     ("bf16", [9000], 12, 512, 64), ("bf16", [9500], 96, 512, 64), ("bf16", [700] * 26, 96, 256, 64),
     ("bf16", [5000, 40, 7000], 30, 384, 16),
     ("bf16", [900] * 9 + [1], 12, 128, 64), ("bf16", [9000, 100, 200, 300, 50, 60], 96, 256, 64),
-    ("f32", [5000], 12, 256, 64), ("f32", [300] * 20, 3, 128, 64)])
+    ("f32", [5000], 12, 256, 64), ("f32", [300] * 20, 3, 128, 64), ("f32", [5000, 30], 32, 512, 64),
+    ("f32", [700, 3] * 4, 60, 256, 24)])
 def test_attn_long_sequence_is_split_and_joined(dtype, lens, H, rank, page):
     """One sequence or a few over all SMs, by few, some and many CTAs; and the same bits again."""
     x = make(dtype, lens, 1, H, rank, 64, page)
