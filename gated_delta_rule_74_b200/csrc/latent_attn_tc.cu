@@ -19,19 +19,21 @@
 //
 // One CTA an SM, its stretch of tiles as latent_attn.cuh lays it out.  Warps 0 and 2 bring
 // the tiles by TMA into a ring, eight tokens with all their columns a box (so that pages of any
-// multiple of eight do), warp 3 Q; warp 1 issues the MMAs; warps 4..11 do the softmax (two
-// warps a lane quarter of 16 tokens, half of the rows each; a thread holds two tokens and two
-// of every eight rows), the rare rescaling of O^T and the results (thread = value column).
+// multiple of eight do), warp 3 Q; warp 1 issues the scores' MMAs, warp 12 the
+// values'; warps 4..11 do the softmax (two warps a lane quarter of 16 tokens, half of the rows
+// each; a thread holds two tokens and two of every eight rows), the rare rescaling of O^T and the
+// results (thread = value column).
 // The maximum that the weights refer to moves only when a score passes it by 2^8: a tile then
 // needs one vote, no reduction over the tokens, O^T is rescaled a few times a sequence, and
 // the weights stay below 2^8, far inside of bf16 and fp32.  Sums are kept by thread and
 // joined at the end of a block; O^T is added up in fp32 in TMEM (against 64 bits 0.0019 of the
 // output's norm, its own rounding and the weights', with 1M tokens a block, 0.004 with 4M, where
 // what the tensor core cuts off at each of 2^18 additions shows).
-// The scores of tile t + 1 go before the values of tile t when the tile is there before the
-// weights are.  The values' products run over 16 tokens at a time and hand those back to the
-// producers at once.  A wait between MMAs costs their warp 300 to 450 cycles, as long as eight
-// of the MMAs take: a tile costs two.
+// Scores and values are issued by two warps, each of which waits for its own operands alone: one
+// warp for both puts the scores of tile t + 1 before the values of tile t, whose slot then comes
+// free 1100 cycles later (chunk 563 us against 500, 256 sequences 216 against 209, 43 of 96 heads
+// 153 against 145).  The values' products run over 16 tokens at a time and hand those back to
+// the producers at once.
 //
 // Rows of the tile that some query row does not see (the causal edge, what lies behind the
 // length in the last page) have weights of exactly zero; their infinities and NaN would
@@ -50,12 +52,12 @@ namespace {
 using namespace sm100;
 using bf16 = __nv_bfloat16;
 
-constexpr int kTcThreads = 384;
+constexpr int kTcThreads = 416;
 constexpr int kSoft = 256;                         // threads of warps 4..11
 constexpr int kTcMaxRows = 96;
 constexpr int kMaxTiles = 4;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kWaitLimit = 1u << 22, kPollLimit = 1u << 26, kDrainLimit = 1u << 14;
+constexpr uint32_t kWaitLimit = 1u << 22, kDrainLimit = 1u << 14;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kNone = -3e38f;                    // maximum of a row that has seen nothing
 
@@ -98,9 +100,9 @@ TcPlan tc_plan(int nr, int rank, int rope) {
 struct TcBars {
   uint64_t q_full[2], q_empty[2];
   uint64_t full[kMaxTiles], empty[kMaxTiles][4];   // empty: by 16 tokens of the tile
-  uint64_t s_full[2], s_empty;
+  uint64_t s_full[2], s_empty[2];
   uint64_t p_full[2], pv_done[2];
-  uint64_t o_empty, drain;
+  uint64_t o_empty, drain[2];
 };
 
 __device__ __forceinline__ float ex2(float x) {      // 2^x; 0 below 2^-126
@@ -152,16 +154,16 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
       mbar_init(&bar.q_full[i], 1);
       mbar_init(&bar.q_empty[i], 1);
       mbar_init(&bar.s_full[i], 1);
+      mbar_init(&bar.s_empty[i], kSoft / 32);
       mbar_init(&bar.p_full[i], kSoft / 32);
       mbar_init(&bar.pv_done[i], 1);
+      mbar_init(&bar.drain[i], 1);
     }
     for (int i = 0; i < kMaxTiles; ++i) {
       mbar_init(&bar.full[i], KK);
       for (int k = 0; k < 4; ++k) mbar_init(&bar.empty[i][k], 1);
     }
-    mbar_init(&bar.s_empty, kSoft / 32);
     mbar_init(&bar.o_empty, kSoft / 32);
-    mbar_init(&bar.drain, 1);
     fence_mbar_init();
     pt.head[blockIdx.x] = make_int4(0, 0, 0, 0);
   }
@@ -244,116 +246,99 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
       if (uses) mbar_wait(&bar.q_full[i], (uses - 1) & 1, kDrainLimit);
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------------- the MMAs
+    // ------------------------------------------------------------- the scores' MMAs
     // The whole warp runs the loop, one lane issues (see elect_one).
     const uint32_t id_qk = idesc_bf16(64, nr, false, false);
-    const uint32_t id_pv = idesc_bf16(128, nr, true, true);
     // first descriptors.  The tile's groups of eight tokens lie `group` bytes apart, as the
-    // rows of the scores' operand and as the K index of the values'; a K step of the scores
-    // is 32 bytes further in a chunk, of the values two groups, of P 512 bytes
+    // rows of this operand; a K step is 32 bytes further in a chunk
     const uint64_t dq = desc_kmajor_sw128(smem_u32(sq), nr, 0);
     const uint64_t dk = smem_desc(smem_u32(ring), 16, pl.group, kSw128);
-    const uint64_t dv = smem_desc(smem_u32(ring), 1024, pl.group, kSw128);
-    const uint64_t dp = desc_mnmajor_sw32(smem_u32(sp), KT, 0);
     LatentWalk walk(st);
     LatentPiece p;
-    uint32_t it = 0, g = 0;                              // blocks, tiles
-    uint32_t slot = 0, use = 0, vslot = 0;               // of the next scores and values
+    uint32_t t = 0, slot = 0, use = 0;                   // tiles
     uint32_t qi = 0, quse = 0;
-    // the scores of tile `t` (it is there)
-    auto issue_qk = [&](uint32_t t, uint64_t q0) {
-      const uint32_t d = tb + kTmemS + (kSBuf == 2 ? t & 1 : 0) * nr;
-      const uint64_t k0 = dk + (uint64_t)(slot * (pl.tile_bytes / 16));
-      if (elect_one()) {
-        for (int c = 0; c < pl.nch; ++c) {
-          const uint64_t a = k0 + (uint64_t)(c * 64), b = q0 + (uint64_t)(c * nr * 8);
-          mma_ss_all(d, a, b, id_qk, c > 0);
-#pragma unroll
-          for (int i = 1; i < 4; ++i) mma_ss_all(d, a + 2 * i, b + 2 * i, id_qk, 1);
-        }
-        mma_commit(&bar.s_full[kSBuf == 2 ? t & 1 : 0]);
-      }
-      __syncwarp();
-      if (++slot == (uint32_t)pl.ntile) {
-        slot = 0;
-        ++use;
-      }
-    };
-    // one score buffer: whether tile t - 1 has been read from it
-    auto s_free = [&](uint32_t t) {
-      if (kSBuf == 2 || t == 0) return true;
-      const bool f = __all_sync(kAll, mbar_test_wait(&bar.s_empty, (t - 1) & 1));
-      if (f) tc_fence_after();
-      return f;
-    };
-
     while (ok && walk.next(sh, seq_lens, cu_seqlens, nr, KT, kLead, &p)) {
       const uint64_t q0 = dq + (uint64_t)(qi * (pl.q_bytes / 16));
-      const int nt = p.t1 - p.t0;
       ok = __all_sync(kAll, mbar_wait(&bar.q_full[qi], quse & 1, kWaitLimit));
-      for (int i = 0; i <= nt && ok; ++i) {
-        // scores of tile i (g + 1 for i > 0) and, before or after them, the values of tile i - 1,
-        // whichever can go first.  With two score buffers the place was read by the softmax of
-        // the tile before last, whose weights have been used; with one, by the last tile's.
-        const uint32_t ts = i == 0 ? g : g + 1;
-        bool scores = i < nt;
-        if (i > 0) {
-          const uint32_t pb = pl.np == 2 ? g & 1 : 0, ppar = (pl.np == 2 ? g >> 1 : g) & 1;
-          for (uint32_t polls = 0; ok; ++polls) {
-            if (!scores) {                               // nothing else can be done before
-              ok = __all_sync(kAll, mbar_wait(&bar.p_full[pb], ppar, kWaitLimit));
-              break;
-            }
-            if (__all_sync(kAll, mbar_test_wait(&bar.p_full[pb], ppar))) break;
-            if (s_free(ts) && __all_sync(kAll, mbar_test_wait(&bar.full[slot], use & 1))) {
-              issue_qk(ts, q0);
-              scores = false;
-            }
-            if (polls > kPollLimit) ok = false;
-          }
-          if (ok && i == 1 && it > 0)                    // the block before has left O^T
-            ok = __all_sync(kAll, mbar_wait(&bar.o_empty, (it - 1) & 1, kWaitLimit));
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t a0 = dv + (uint64_t)(vslot * (pl.tile_bytes / 16));
-          const uint64_t b0 = dp + (uint64_t)(pb * (pl.p_bytes / 16));
-          if (elect_one()) {
+      for (int i = p.t0; i < p.t1 && ok; ++i, ++t) {
+        const uint32_t sb = t % kSBuf;
+        bool go = mbar_wait(&bar.full[slot], use & 1, kWaitLimit);
+        if (t >= kSBuf) go = go && mbar_wait(&bar.s_empty[sb], (t / kSBuf - 1) & 1, kWaitLimit);
+        ok = __all_sync(kAll, go);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t d = tb + kTmemS + sb * nr;
+        const uint64_t k0 = dk + (uint64_t)(slot * (pl.tile_bytes / 16));
+        if (elect_one()) {
+          for (int c = 0; c < pl.nch; ++c) {
+            const uint64_t a = k0 + (uint64_t)(c * 64), b = q0 + (uint64_t)(c * nr * 8);
+            mma_ss_all(d, a, b, id_qk, c > 0);
 #pragma unroll
-            for (int k = 0; k < KK; ++k) {
-              const uint64_t a = a0 + (uint64_t)(2 * k * (pl.group / 16));
-              for (int j = 0; j < npair; ++j)
-                mma_ss_all(tb + j * nr, a + (uint64_t)(j * 128), b0 + 32 * k, id_pv, k > 0 || i > 1);
-              mma_commit(&bar.empty[vslot][k]);
-            }
-            mma_commit(&bar.pv_done[pb]);
+            for (int e = 1; e < 4; ++e) mma_ss_all(d, a + 2 * e, b + 2 * e, id_qk, 1);
           }
-          __syncwarp();
-          if (++vslot == (uint32_t)pl.ntile) vslot = 0;
-          ++g;
+          mma_commit(&bar.s_full[sb]);
+          if (i == p.t1 - 1) mma_commit(&bar.q_empty[qi]);
         }
-        if (scores) {
-          if (kSBuf == 1 && ts > 0) {
-            ok = __all_sync(kAll, mbar_wait(&bar.s_empty, (ts - 1) & 1, kWaitLimit));
-            tc_fence_after();
-          }
-          ok = ok && __all_sync(kAll, mbar_wait(&bar.full[slot], use & 1, kWaitLimit));
-          if (ok) issue_qk(ts, q0);
-        }
-        if (i == nt - 1 && ok) {
-          if (elect_one()) mma_commit(&bar.q_empty[qi]);
-          __syncwarp();
+        __syncwarp();
+        if (++slot == (uint32_t)pl.ntile) {
+          slot = 0;
+          ++use;
         }
       }
-      ++it;
       if (++qi == (uint32_t)pl.nq) {
         qi = 0;
         ++quse;
       }
     }
     if (!ok) {
-      if (elect_one()) mma_commit(&bar.drain);
+      if (elect_one()) mma_commit(&bar.drain[0]);
       __syncwarp();
-      mbar_wait(&bar.drain, 0, kWaitLimit);
+      mbar_wait(&bar.drain[0], 0, kWaitLimit);
+    }
+  } else if (warp == 12) {
+    // ------------------------------------------------------------- the values' MMAs
+    const uint32_t id_pv = idesc_bf16(128, nr, true, true);
+    // the groups of eight tokens are the K index of this operand, a K step two groups; of P
+    // 512 bytes
+    const uint64_t dv = smem_desc(smem_u32(ring), 1024, pl.group, kSw128);
+    const uint64_t dp = desc_mnmajor_sw32(smem_u32(sp), KT, 0);
+    LatentWalk walk(st);
+    LatentPiece p;
+    uint32_t it = 0, slot = 0;                           // blocks; tile of the ring
+    uint32_t pb = 0, puse = 0;
+    while (ok && walk.next(sh, seq_lens, cu_seqlens, nr, KT, kLead, &p)) {
+      for (int i = p.t0; i < p.t1; ++i) {
+        bool go = mbar_wait(&bar.p_full[pb], puse & 1, kWaitLimit);
+        if (i == p.t0 && it > 0)                         // the block before has left O^T
+          go = go && mbar_wait(&bar.o_empty, (it - 1) & 1, kWaitLimit);
+        ok = __all_sync(kAll, go);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t a0 = dv + (uint64_t)(slot * (pl.tile_bytes / 16));
+        const uint64_t b0 = dp + (uint64_t)(pb * (pl.p_bytes / 16));
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < KK; ++k) {
+            const uint64_t a = a0 + (uint64_t)(2 * k * (pl.group / 16));
+            for (int j = 0; j < npair; ++j)
+              mma_ss_all(tb + j * nr, a + (uint64_t)(j * 128), b0 + 32 * k, id_pv, k > 0 || i > p.t0);
+            mma_commit(&bar.empty[slot][k]);
+          }
+          mma_commit(&bar.pv_done[pb]);
+        }
+        __syncwarp();
+        if (++slot == (uint32_t)pl.ntile) slot = 0;
+        if (++pb == (uint32_t)pl.np) {
+          pb = 0;
+          ++puse;
+        }
+      }
+      ++it;
+    }
+    if (!ok) {
+      if (elect_one()) mma_commit(&bar.drain[1]);
+      __syncwarp();
+      mbar_wait(&bar.drain[1], 0, kWaitLimit);
     }
   } else {
     // ------------------------------------------------------------- softmax and results
@@ -399,10 +384,8 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
           tmem_wait_ld();
         }
         tc_fence_before();
-        if (kSBuf == 1) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar.s_empty);
-        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.s_empty[sb]);
         // whether some scaled score passes its row's maximum by 2^8
         float top = -INFINITY;
         if (act && mixed) {
