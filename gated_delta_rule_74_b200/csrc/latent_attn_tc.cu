@@ -61,11 +61,11 @@ constexpr uint32_t kWaitLimit = 1u << 22, kDrainLimit = 1u << 14;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kNone = -3e38f;                    // maximum of a row that has seen nothing
 
-// Tokens of a tile.  64 fill the MMAs' M side; 48 where only one tile of 64 would fit beside Q
-// (148 sequences of 8192 tokens and 96 heads: 401 us against 419 with one and a half).  At 48
-// rows three tiles of 48 would fit, but two of 64 are faster (85 us against 92 for four
-// drafts of 64 sequences), and so at 16 rows (219 against 234 us for 256 sequences).
-__host__ __device__ constexpr int tc_tile(int nr) { return nr >= 80 ? 48 : 64; }
+// Tokens of a tile.  64 fill the MMAs' M side, but there is room for more tiles of 48 beside Q at
+// rank 512: three instead of two up to 48 rows (256 sequences of 12 heads 203 us against 209, 100 of
+// 24 heads 96 against 98), two instead of one at 80 and 96 (60 of 80 heads 103 against 128).  Of
+// either two fit at 64 rows.  Tiles of 32 at 16 rows cost more MMAs than they save (242 us).
+__host__ __device__ constexpr int tc_tile(int nr) { return nr == 64 ? 64 : 48; }
 // Dynamic shared memory: all but 3 KB of the 227 (2 KB at 96 rows) for the variables.
 __host__ __device__ constexpr uint32_t tc_smem(int nr) { return nr > 80 ? 230400 : 229376; }
 
@@ -78,7 +78,7 @@ struct TcPlan {
   uint32_t group, tile_bytes, q_bytes, p_bytes;
 };
 
-// Q is buffered twice while it is small (a decode step changes blocks every few tiles), P
+// Q is buffered twice while that costs no tile (a decode step changes blocks every few tiles), P
 // where there is room beside the tiles.
 TcPlan tc_plan(int nr, int rank, int rope) {
   TcPlan p;
@@ -89,7 +89,7 @@ TcPlan tc_plan(int nr, int rank, int rope) {
   p.tile_bytes = kt / 8 * p.group;
   p.q_bytes = (uint32_t)nr * p.nch * 128;
   p.p_bytes = (uint32_t)nr * kt * 2;
-  p.nq = nr <= 32 ? 2 : 1;
+  p.nq = nr <= 16 ? 2 : 1;
   const uint32_t fixed = p.nq * p.q_bytes + p.p_bytes;
   p.ntile = (int)((tc_smem(nr) - fixed) / p.tile_bytes);
   if (p.ntile > kMaxTiles) p.ntile = kMaxTiles;
@@ -126,7 +126,8 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                      const int32_t* __restrict__ cu_seqlens, bf16* __restrict__ out,
                      float* __restrict__ lse, LatentAttnShape sh, TcPlan pl, LatentPartials pt) {
   constexpr int nr = NR, KT = tc_tile(NR), KK = KT / 16, kSBuf = NR <= 80 ? 2 : 1;
-  constexpr int kLead = NR <= 48 ? 2 : 3;           // tiles that a block costs besides its own
+  // tiles that a block costs besides its own (193 sequences of 3 blocks: 124 us, 133 with 2 and 3)
+  constexpr int kLead = NR <= 48 ? 3 : 5;
   constexpr uint32_t kTmemS = 4 * NR;
   // the alignment is part of the declaration: there is no room to round up
   extern __shared__ __align__(1024) uint8_t sm[];
@@ -149,24 +150,17 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
     tmem_alloc(&s_tmem, kTmemCols);
     tmem_relinquish();
   }
-  if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&bar.q_full[i], 1);
-      mbar_init(&bar.q_empty[i], 1);
-      mbar_init(&bar.s_full[i], 1);
-      mbar_init(&bar.s_empty[i], kSoft / 32);
-      mbar_init(&bar.p_full[i], kSoft / 32);
-      mbar_init(&bar.pv_done[i], 1);
-      mbar_init(&bar.drain[i], 1);
+  {                                                 // a barrier a thread
+    uint64_t* const mine = reinterpret_cast<uint64_t*>(&bar) + tid;
+    if (tid < (int)(sizeof(bar) / sizeof(uint64_t))) {
+      const bool soft = mine == &bar.o_empty || (mine >= bar.s_empty && mine < bar.s_empty + 2) ||
+                        (mine >= bar.p_full && mine < bar.p_full + 2);
+      const bool tile = mine >= bar.full && mine < bar.full + kMaxTiles;
+      mbar_init(mine, soft ? kSoft / 32 : tile ? KK : 1);
+      fence_mbar_init();
     }
-    for (int i = 0; i < kMaxTiles; ++i) {
-      mbar_init(&bar.full[i], KK);
-      for (int k = 0; k < 4; ++k) mbar_init(&bar.empty[i][k], 1);
-    }
-    mbar_init(&bar.o_empty, kSoft / 32);
-    fence_mbar_init();
-    pt.head[blockIdx.x] = make_int4(0, 0, 0, 0);
   }
+  if (tid == 96) pt.head[blockIdx.x] = make_int4(0, 0, 0, 0);
   latent_find_start(sh, seq_lens, cu_seqlens, nr, KT, kLead, &st,
                     reinterpret_cast<long long*>(s_red));
   tc_fence_before();
@@ -613,15 +607,15 @@ TcKernel tc_kernel(int nr) {
 
 // Rows of a block: all of a sequence's up to 64, a multiple of 16.  Up to 96: all of them, or, of
 // few sequences, two blocks of 48: the CTAs then share a sequence by many, and what they
-// write and join counts for more than reading the cache twice (96 heads, 6000 tokens: 4
-// sequences 31 us against 41, 24 sequences 71 against 73, 43 of up to 16384 tokens 182 against
-// 152).  Of more rows, 64, whose tiles of 64 tokens cost the MMAs less a row and token than
-// 96 with tiles of 48 (a 1024-token chunk of 12 heads behind 8192 to 32768 tokens: 562 us
-// against 635).
+// write and join counts for more than reading the cache twice (96 heads, 4000 to 8192 tokens: 4
+// sequences 34 us against 42, 16 58 against 65, 24 79 either way; 43 of up to 16384 160 against
+// 146).  Of more rows, 64, whose tiles of 64 tokens cost the MMAs less a row and token than
+// 96 or 48 with tiles of 48 (a 1024-token chunk of 12 heads behind 8192 to 32768 tokens: 507 us
+// against 541 and 539).
 int tc_rows(int N, int L, int T, int H) {
   const long long rows = L > 0 ? (long long)L * H : (((long long)T + N - 1) / N) * H;
   if (rows > kTcMaxRows) return 64;
-  if (rows > 64 && N <= 24) return 48;
+  if (rows > 64 && N <= 16) return 48;
   return (int)((rows + 15) / 16 * 16);
 }
 
