@@ -537,14 +537,22 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
       named_bar(1, kSoft);
       tc_fence_after();
       // 16 rows a load, the next one's under the stores: each stores 32 columns of a row a warp
-      const int nc = (p.rows + 15) / 16, n = nc * ((npair - half + 1) / 2);
       uint32_t o[2][16];
-      auto fetch = [&](int u, uint32_t (&v)[16]) {       // u-th of this warp's loads
-        tmem_ld16(tl + (half + 2 * (u / nc)) * nr + 16 * (u % nc), v);
+      int fi = 0, fj = half, si = 0, sj = half;          // row and columns of the next load, store
+      auto step = [&](int& i, int& j) {
+        i += 16;
+        if (i >= p.rows) {
+          i = 0;
+          j += 2;
+        }
       };
-      auto put = [&](int u, const uint32_t (&v)[16]) {
-        const int i = 16 * (u % nc), d = 128 * (half + 2 * (u / nc)) + 32 * wq + lane;
-        const int rows = min(p.rows - i, 16);
+      auto fetch = [&](uint32_t (&v)[16]) {
+        if (fj < npair) tmem_ld16(tl + fj * nr + fi, v);
+        step(fi, fj);
+      };
+      auto put = [&](const uint32_t (&v)[16]) {
+        const int i = si, d = 128 * sj + 32 * wq + lane, rows = min(p.rows - i, 16);
+        step(si, sj);
         float f[16];
 #pragma unroll
         for (int e = 0; e < 16; e += 4) {
@@ -566,16 +574,16 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
             if (e < rows) *y = f[e];
         }
       };
-      if (n > 0) fetch(0, o[0]);
+      fetch(o[0]);
 #pragma unroll 1
-      for (int u = 0; u < n; u += 2) {
+      while (sj < npair) {
         tmem_wait_ld();
-        if (u + 1 < n) fetch(u + 1, o[1]);
-        put(u, o[0]);
-        if (u + 1 >= n) break;
+        fetch(o[1]);
+        put(o[0]);
+        if (sj >= npair) break;
         tmem_wait_ld();
-        if (u + 2 < n) fetch(u + 2, o[0]);
-        put(u + 1, o[1]);
+        fetch(o[0]);
+        put(o[1]);
       }
       tc_fence_before();
       named_bar(1, kSoft);                               // the block's rows are done with
