@@ -264,6 +264,15 @@ def _stream(stream) -> int:
     return _raw_stream(torch.cuda.current_device()) if stream is None else stream.cuda_stream
 
 
+def _new(stream, like: torch.Tensor, shape, dtype) -> torch.Tensor:
+    """An output that the call writes on `stream`: its memory comes from that stream's pool, as
+    memory of the current stream's may still be in use there."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
+
+
 def _check(name: str, t: torch.Tensor, dtype=None, shape=None):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -310,10 +319,10 @@ def kda_chunk_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Te
     if h0 is not None:
         _check("h0", h0, torch.float32, (nseq, H, dk, dv))
     if out is None:
-        out = torch.empty((Bt, T, H, dv), dtype=q.dtype, device=q.device)
+        out = _new(stream, q, (Bt, T, H, dv), q.dtype)
     _check("out", out, q.dtype, (Bt, T, H, dv))
     if hT is None and output_final_state:
-        hT = torch.empty((nseq, H, dk, dv), dtype=torch.float32, device=q.device)
+        hT = _new(stream, q, (nseq, H, dk, dv), torch.float32)
     if hT is not None:
         _check("hT", hT, torch.float32, (nseq, H, dk, dv))
     if noalloc and G != 1:
@@ -382,10 +391,10 @@ def kda_chunk_fwd_fused(q_raw: torch.Tensor, k_raw: torch.Tensor, v: torch.Tenso
     if h0 is not None:
         _check("h0", h0, torch.float32, (nseq, H, dk, dv))
     if out is None:
-        out = torch.empty((Bt, T, H, dv), dtype=q_raw.dtype, device=q_raw.device)
+        out = _new(stream, q_raw, (Bt, T, H, dv), q_raw.dtype)
     _check("out", out, q_raw.dtype, (Bt, T, H, dv))
     if hT is None and output_final_state:
-        hT = torch.empty((nseq, H, dk, dv), dtype=torch.float32, device=q_raw.device)
+        hT = _new(stream, q_raw, (nseq, H, dk, dv), torch.float32)
     if hT is not None:
         _check("hT", hT, torch.float32, (nseq, H, dk, dv))
     rc = lib().kda_chunk_fwd_fused(_ptr(q_raw), _ptr(k_raw), _ptr(v), _ptr(conv_q), _ptr(conv_k),
@@ -442,7 +451,7 @@ def kda_chunk_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Te
             res[name] = None
             continue
         if res.get(name) is None:
-            res[name] = torch.empty(shp, dtype=torch.float32, device=q.device)
+            res[name] = _new(stream, q, shp, torch.float32)
         _check(name, res[name], torch.float32, shp)
     args = [_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(h0), _ptr(cu_seqlens),
             _ptr(dout), _ptr(dhT), _ptr(res["dq"]), _ptr(res["dk"]), _ptr(res["dv"]),
@@ -488,7 +497,7 @@ def kda_decode_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.
     _check("beta", beta, torch.float32, (N, H))
     _check("S", S, torch.float32, (N, H, dk, dv))
     if out is None:
-        out = torch.empty((N, H, dv), dtype=q.dtype, device=q.device)
+        out = _new(stream, q, (N, H, dv), q.dtype)
     _check("out", out, q.dtype, (N, H, dv))
     rc = lib().kda_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S),
                                _ptr(out), N, H, dk, dv, dt, _stream(stream))
@@ -519,7 +528,7 @@ def kda_decode_tokens(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torc
     _check("beta", beta, torch.float32, (N, L, H))
     _check("S", S, torch.float32, (N, H, dk, dv))
     if out is None:
-        out = torch.empty((N, L, H, dv), dtype=q.dtype, device=q.device)
+        out = _new(stream, q, (N, L, H, dv), q.dtype)
     _check("out", out, q.dtype, (N, L, H, dv))
     if G == 1:
         rc = lib().kda_decode_tokens(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S),
@@ -553,7 +562,7 @@ def kda_decode_chunk(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch
     _check("beta", beta, torch.float32, (N, L, H))
     _check("S", S, torch.float32, (N, H, dk, dv))
     if out is None:
-        out = torch.empty((N, L, H, dv), dtype=q.dtype, device=q.device)
+        out = _new(stream, q, (N, L, H, dv), q.dtype)
     _check("out", out, q.dtype, (N, L, H, dv))
     rc = lib().kda_decode_chunk(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S),
                                 _ptr(out), N, L, H, dk, dv, dt, _stream(stream))
@@ -580,15 +589,6 @@ def _device_of(name: str, t: torch.Tensor) -> int:
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     return t.get_device()
-
-
-def _new(stream, like: torch.Tensor, shape, dtype) -> torch.Tensor:
-    """An output that the call writes on `stream`: its memory comes from that stream's pool, as
-    memory of the current stream's may still be in use there."""
-    if stream is None:
-        return like.new_empty(shape, dtype=dtype)
-    with torch.cuda.stream(stream):
-        return like.new_empty(shape, dtype=dtype)
 
 
 def _take(name: str, t: Optional[torch.Tensor], dev: int, dtype, shape) -> Optional[int]:
