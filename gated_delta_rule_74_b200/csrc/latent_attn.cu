@@ -509,9 +509,10 @@ cudaError_t run_simt(const void* q, const void* cache, const int32_t* page_table
 
 }  // namespace
 
-// `items`: blocks of rows of the call (packed: about).  Few of them, each over more than 16
+// `items`: blocks of rows of the call (packed: at most).  Few of them, each over more than 16
 // CTAs, are listed and spread over the grid, two rounds at most of 2 us (8 sequences of 16 heads,
-// rank 128: 15.7 us a call against 17.7); a warp for each 128 columns of a row where some
+// rank 128: 15.7 us a call against 17.7; a list of many is slow: 100 sequences of one head behind
+// 500 tokens 55 us against 22); a warp for each 128 columns of a row where some
 // CTAs share it (16 sequences of 12 heads: 27.0 against 30.8 listed); else blocks of 8 rows, of
 // which many find nothing to do.
 cudaError_t launch_latent_join(void* out, float* lse, const LatentPartials& pt, int G, int nr,
@@ -535,8 +536,9 @@ cudaError_t launch_latent_join(void* out, float* lse, const LatentPartials& pt, 
 }
 
 long long latent_items(const LatentAttnShape& sh, int nr) {
+  // packed: the whole blocks that there can be, and one more for each sequence with tokens
   return sh.L > 0 ? sh.N * (((long long)sh.L * sh.H + nr - 1) / nr)
-                  : ((long long)sh.T * sh.H + nr - 1) / nr;
+                  : (long long)sh.T * sh.H / nr + (sh.N < sh.T ? sh.N : sh.T);
 }
 
 size_t latent_attn_scratch_bytes(int N, int L, int T, int H, int rank, int rope, int page_size,

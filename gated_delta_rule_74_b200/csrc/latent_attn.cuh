@@ -63,7 +63,7 @@ cudaError_t launch_latent_tc(const void* q, const void* cache, const int32_t* pa
                              cudaStream_t stream);
 cudaError_t launch_latent_join(void* out, float* lse, const LatentPartials& pt, int G, int nr,
                                int rank, long long items, int dtype, cudaStream_t stream);
-// Blocks of nr rows of a call (packed: at least).
+// Blocks of nr rows of a call (packed: at most).
 long long latent_items(const LatentAttnShape& sh, int nr);
 
 // ------------------------------------------------------------------ device side

@@ -1,0 +1,52 @@
+"""Packed latent attention calls whose sequences are unlike: against the float64 reference of
+oracle/latent.py, and against the same work given in another form."""
+import statistics
+
+import pytest
+import torch
+
+import gated_delta_rule_74_b200 as kda
+from test_gpu_latent import call, close, make
+
+pytestmark = pytest.mark.gpu
+
+
+def device_us(fn, calls=6):
+    """Median time of a call on the device, from replays of a graph of several."""
+    for _ in range(3):
+        fn()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for _ in range(calls):
+            fn()
+    times = []
+    for _ in range(12):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        g.replay()
+        b.record()
+        torch.cuda.synchronize()
+        times.append(a.elapsed_time(b) / calls * 1e3)
+    return statistics.median(times[3:])
+
+
+@pytest.mark.parametrize("dtype,n,H,rank", [("bf16", 100, 1, 512), ("bf16", 60, 1, 512), ("f32", 40, 2, 128)])
+def test_one_token_sequences_packed_as_uniform(dtype, n, H, rank):
+    """One new token a sequence, packed or not: the same work (and join, so the same bits). The
+    packed call's blocks are one a sequence too, not as many as the rows would fill (which spent
+    55 us on the join of 100 sequences behind 500 tokens, for 22; half as much again is allowed)."""
+    x = make(dtype, [500] * n, 1, H, rank, 64, 64)
+    out, lse = call(x)
+    d = {k: (v.cuda() if isinstance(v, torch.Tensor) else v) for k, v in x.items()}
+    q = d["q"].reshape(1, n, H, rank + 64)
+    cu = torch.arange(n + 1, dtype=torch.int32, device="cuda")
+    args = (d["cache"], d["table"], d["lens"])
+    kw = dict(rank=rank, scale=x["scale"])
+    po, pz = kda.kda_latent_attn(q, *args, cu_seqlens=cu, **kw)
+    torch.cuda.synchronize()
+    close(x, out, lse)
+    assert torch.equal(po.reshape(out.shape), out) and torch.equal(pz.reshape(lse.shape), lse)
+    uniform = device_us(lambda: kda.kda_latent_attn(d["q"], *args, **kw))
+    packed = device_us(lambda: kda.kda_latent_attn(q, *args, cu_seqlens=cu, **kw))
+    assert packed <= 1.5 * uniform, (packed, uniform)
