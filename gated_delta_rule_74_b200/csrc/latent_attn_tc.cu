@@ -620,10 +620,17 @@ TcKernel tc_kernel(int nr) {
 // 146).  Of more rows, 64, whose tiles of 64 tokens cost the MMAs less a row and token than
 // 96 or 48 with tiles of 48 (a 1024-token chunk of 12 heads behind 8192 to 32768 tokens: 507 us
 // against 541 and 539).
+// Packed, a sequence has so many on average, which says little when one has most of them: from 1024
+// rows on that are more than a token for each sequence, at least 48 (512 slots, all empty but for
+// a 1024-token chunk of 12 heads behind 16384: 32 rows 804 us, 48 594, 64 553; 256 sequences of two
+// tokens behind 4000, which the host cannot tell from it: 220, 233, 276).  Fewer tokens than sequences are
+// a decode batch with empty slots: 16 rows of 12 heads 210 us, 48 222.
+constexpr int kTcSkewRows = 1024;
 int tc_rows(int N, int L, int T, int H) {
   const long long rows = L > 0 ? (long long)L * H : (((long long)T + N - 1) / N) * H;
   if (rows > kTcMaxRows) return 64;
   if (rows > 64 && N <= 16) return 48;
+  if (L == 0 && rows < 48 && ((long long)T - N + 1) * H >= kTcSkewRows) return 48;
   return (int)((rows + 15) / 16 * 16);
 }
 

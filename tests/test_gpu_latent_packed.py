@@ -50,3 +50,18 @@ def test_one_token_sequences_packed_as_uniform(dtype, n, H, rank):
     uniform = device_us(lambda: kda.kda_latent_attn(d["q"], *args, **kw))
     packed = device_us(lambda: kda.kda_latent_attn(q, *args, cu_seqlens=cu, **kw))
     assert packed <= 1.5 * uniform, (packed, uniform)
+
+
+@pytest.mark.parametrize("dtype,H", [("bf16", 12), ("bf16", 3), ("f32", 4)])
+def test_one_long_chunk_among_empty_and_one_token_sequences(dtype, H):
+    """Most rows in one sequence, in the middle, at the end and at the start of the batch."""
+    for at, others in ((20, 0), (40, 1), (0, 1)):
+        new = [others] * 41
+        new[at] = 400
+        cu = [0]
+        for n in new:
+            cu.append(cu[-1] + n)
+        lens = [90 + 3 * n if c else 0 for n, c in enumerate(new)]
+        lens[at] = 450
+        x = make(dtype, lens, cu[-1], H, 128, 64, 64, cu=cu, seed=at + others)
+        close(x, *call(x))
