@@ -129,6 +129,8 @@ def lib() -> ctypes.CDLL:
         L.kda_latent_attn.restype = ctypes.c_int
         L.kda_latent_attn_ws.argtypes = L.kda_latent_attn.argtypes[:-1] + [vp, sz, vp]
         L.kda_latent_attn_ws.restype = ctypes.c_int
+        L.kda_selftest_latent_waits.argtypes = [ctypes.c_uint, *L.kda_latent_attn.argtypes[:-2], vp]
+        L.kda_selftest_latent_waits.restype = ctypes.c_int
         L.kda_latent_attn_workspace_size.argtypes = [ip] * 9 + [ctypes.POINTER(sz)]
         L.kda_latent_attn_workspace_size.restype = ctypes.c_int
         L.kda_verify_tokens.argtypes = [vp] * 7 + [ip] * 3 + [vp]

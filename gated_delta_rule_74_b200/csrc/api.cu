@@ -336,7 +336,8 @@ int latent_attn_impl(const void* q, const void* kv_cache, const int32_t* page_ta
                      const int32_t* seq_lens, const int32_t* cu_seqlens, void* out, float* lse,
                      int N, int L, int H, int rank, int rope, int num_pages, int page_size,
                      int max_pages, long long page_stride, long long row_stride, float scale,
-                     int dtype, void* stream, const kda::Workspace* ws) {
+                     int dtype, void* stream, const kda::Workspace* ws,
+                     uint32_t polls = kda::kLatentPolls) {
   const int rc = latent_shape_ok(N, L, H, rank, rope, num_pages, page_size, max_pages, page_stride,
                                  row_stride, dtype, cu_seqlens != nullptr);
   if (rc != KDA_OK) return rc;
@@ -359,7 +360,7 @@ int latent_attn_impl(const void* q, const void* kv_cache, const int32_t* page_ta
   if (L == 0) return KDA_OK;                        // no new tokens: nothing to write
   return status_from(kda::launch_latent_attn(q, kv_cache, page_table, seq_lens, cu_seqlens, out,
                                              lse, sh, dtype, static_cast<cudaStream_t>(stream),
-                                             ws));
+                                             ws, polls));
 }
 }  // namespace
 
@@ -433,6 +434,18 @@ int kda_latent_attn_ws(const void* q, const void* kv_cache, const int32_t* page_
   return latent_attn_impl(q, kv_cache, page_table, seq_lens, cu_seqlens, out, lse, N, L, H, rank,
                           rope, num_pages, page_size, max_pages, page_stride, row_stride, scale,
                           dtype, stream, &ws);
+}
+
+int kda_selftest_latent_waits(unsigned polls, const void* q, const void* kv_cache,
+                              const int32_t* page_table, const int32_t* seq_lens,
+                              const int32_t* cu_seqlens, void* out, float* lse, int N, int L, int H,
+                              int rank, int rope, int num_pages, int page_size, int max_pages,
+                              long long page_stride, long long row_stride, float scale,
+                              void* stream) {
+  if (polls > (1u << 20) || page_size % 8 != 0) return KDA_ERR_INVALID_ARG;
+  return latent_attn_impl(q, kv_cache, page_table, seq_lens, cu_seqlens, out, lse, N, L, H, rank,
+                          rope, num_pages, page_size, max_pages, page_stride, row_stride, scale,
+                          KDA_BF16, stream, nullptr, polls);
 }
 
 int kda_latent_attn_workspace_size(int N, int L, int H, int rank, int rope, int page_size,

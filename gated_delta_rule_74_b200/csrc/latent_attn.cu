@@ -552,7 +552,7 @@ size_t latent_attn_scratch_bytes(int N, int L, int T, int H, int rank, int rope,
 cudaError_t launch_latent_attn(const void* q, const void* cache, const int32_t* page_table,
                                const int32_t* seq_lens, const int32_t* cu_seqlens, void* out,
                                float* lse, const LatentAttnShape& sh, int dtype,
-                               cudaStream_t stream, const Workspace* ws) {
+                               cudaStream_t stream, const Workspace* ws, uint32_t polls) {
   int sms = 0;
   cudaMemPool_t pool = nullptr;
   if (!device_ctx(&sms, ws ? nullptr : &pool)) return cudaErrorInvalidDevice;
@@ -573,7 +573,8 @@ cudaError_t launch_latent_attn(const void* q, const void* cache, const int32_t* 
   const int G = simt_ctas(sms, D, sh.rank, dtype);
   const LatentPartials pt = latent_partials(buf, G, rows);
   if (latent_tc_supported(dtype, sh.page_size))
-    e = launch_latent_tc(q, cache, page_table, seq_lens, cu_seqlens, out, lse, sh, sms, buf, stream);
+    e = launch_latent_tc(q, cache, page_table, seq_lens, cu_seqlens, out, lse, sh, sms, buf, stream,
+                         polls);
   else
     e = dtype == KDA_BF16 ? run_simt<__nv_bfloat16>(q, cache, page_table, seq_lens, cu_seqlens, out,
                                                   lse, sh, rows, G, pt, stream)

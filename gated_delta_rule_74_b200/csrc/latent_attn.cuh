@@ -32,6 +32,7 @@ struct LatentPartials {
   float* o;                         // [2 G][nr][rank]
 };
 constexpr int kLatentMaxCtas = 1024;
+constexpr uint32_t kLatentPolls = 1u << 22;   // of a wait, before it gives up
 
 inline size_t latent_scratch_bytes(int G, int nr, int rank) {
   return (size_t)kLatentMaxCtas * sizeof(int4) + (((size_t)2 * G * nr * 4 + 255) & ~(size_t)255) +
@@ -52,7 +53,8 @@ size_t latent_attn_scratch_bytes(int N, int L, int T, int H, int rank, int rope,
 cudaError_t launch_latent_attn(const void* q, const void* cache, const int32_t* page_table,
                                const int32_t* seq_lens, const int32_t* cu_seqlens, void* out,
                                float* lse, const LatentAttnShape& sh, int dtype,
-                               cudaStream_t stream, const Workspace* ws);
+                               cudaStream_t stream, const Workspace* ws,
+                               uint32_t polls = kLatentPolls);
 
 // The tensor-core kernel (latent_attn_tc.cu): bf16, pages of a multiple of 8 rows.
 bool latent_tc_supported(int dtype, int page_size);
@@ -60,7 +62,7 @@ size_t latent_tc_scratch_bytes(int N, int L, int T, int H, int rank, int sms);
 cudaError_t launch_latent_tc(const void* q, const void* cache, const int32_t* page_table,
                              const int32_t* seq_lens, const int32_t* cu_seqlens, void* out,
                              float* lse, const LatentAttnShape& sh, int sms, void* buf,
-                             cudaStream_t stream);
+                             cudaStream_t stream, uint32_t polls);
 cudaError_t launch_latent_join(void* out, float* lse, const LatentPartials& pt, int G, int nr,
                                int rank, long long items, int dtype, cudaStream_t stream);
 // Blocks of nr rows of a call (packed: at most).

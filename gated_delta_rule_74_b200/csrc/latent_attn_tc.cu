@@ -22,7 +22,8 @@
 // multiple of eight do), warp 3 Q; warp 1 issues the scores' MMAs, warp 12 the
 // values'; warps 4..11 do the softmax (two warps a lane quarter of 16 tokens, half of the rows
 // each; a thread holds two tokens and two of every eight rows), the rare rescaling of O^T and the
-// results (thread = value column).
+// results (thread = value column).  When a wait of one of them gives up, all of them meet at a
+// barrier, and those with loads or MMAs in flight wait for these before the CTA leaves.
 // The maximum that the weights refer to moves only when a score passes it by 2^8: a tile then
 // needs one vote, no reduction over the tokens, O^T is rescaled a few times a sequence, and
 // the weights stay below 2^8, far inside of bf16 and fp32.  Sums are kept by thread and
@@ -57,7 +58,7 @@ constexpr int kSoft = 256;                         // threads of warps 4..11
 constexpr int kTcMaxRows = 96;
 constexpr int kMaxTiles = 4;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kWaitLimit = 1u << 22, kDrainLimit = 1u << 14;
+constexpr uint32_t kDrainLimit = 1u << 14;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kNone = -3e38f;                    // maximum of a row that has seen nothing
 
@@ -124,7 +125,8 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                      const int32_t* __restrict__ page_table,
                      const int32_t* __restrict__ seq_lens,
                      const int32_t* __restrict__ cu_seqlens, bf16* __restrict__ out,
-                     float* __restrict__ lse, LatentAttnShape sh, TcPlan pl, LatentPartials pt) {
+                     float* __restrict__ lse, LatentAttnShape sh, TcPlan pl, LatentPartials pt,
+                     uint32_t limit) {
   constexpr int nr = NR, KT = tc_tile(NR), KK = KT / 16, kSBuf = NR <= 80 ? 2 : 1;
   // tiles that a block costs besides its own (193 sequences of 3 blocks: 124 us, 133 with 2 and 3)
   constexpr int kLead = NR <= 48 ? 3 : 5;
@@ -139,6 +141,7 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
   // two lane quarters' maxima or sums at a time; before, the sums of latent_find_start
   __shared__ __align__(16) float s_red[2 * NR < 68 ? 68 : 2 * NR];
   __shared__ uint32_t s_tmem;
+  __shared__ uint32_t s_units[2];                   // 16-token loads that warps 0 and 2 have started
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int npair = pl.npair;
   // the ring first: the MMAs' 64 rows of a 48-token tile reach 16 rows behind it, into Q
@@ -177,7 +180,7 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
     // arm, copy; 400 to 600 cycles) alone holds the stream below 4 TB/s.
     LatentWalk walk(st);
     LatentPiece p;
-    uint32_t slot = 0, use = 0, turn = 0;
+    uint32_t slot = 0, use = 0, turn = 0, units = 0;
     while (ok && walk.next(sh, seq_lens, cu_seqlens, nr, KT, kLead, &p)) {
       // lane's group of tile t: its page (one past the cache, which reads as zeros, where there
       // is none)
@@ -194,7 +197,7 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
         uint8_t* const d = ring + slot * pl.tile_bytes;
         for (int k = 0; k < KK; ++k, turn ^= 1) {
           if (turn != (uint32_t)(warp >> 1)) continue;
-          if (use > 0) ok = __all_sync(kAll, mbar_wait(&bar.empty[slot][k], (use - 1) & 1, kWaitLimit));
+          if (use > 0) ok = __all_sync(kAll, mbar_wait(&bar.empty[slot][k], (use - 1) & 1, limit));
           if (!ok) break;
           const int pg0 = __shfl_sync(kAll, page, 2 * k), rw0 = __shfl_sync(kAll, row, 2 * k);
           const int pg1 = __shfl_sync(kAll, page, 2 * k + 1), rw1 = __shfl_sync(kAll, row, 2 * k + 1);
@@ -203,6 +206,7 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
             tma_load_4d(d + 2 * k * pl.group, &c_map, 0, rw0, 0, pg0, &bar.full[slot]);
             tma_load_4d(d + (2 * k + 1) * pl.group, &c_map, 0, rw1, 0, pg1, &bar.full[slot]);
           }
+          ++units;
           __syncwarp();
         }
         if (++slot == (uint32_t)pl.ntile) {
@@ -211,11 +215,19 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
         }
       }
     }
-    // let copies in flight land before the memory goes away (those that never started cost
-    // the limit)
-    for (uint32_t i = 0; !ok && i < (uint32_t)pl.ntile; ++i) {
-      const uint32_t uses = use + (i <= slot ? 1 : 0);
-      if (uses) mbar_wait(&bar.full[i], (uses - 1) & 1, kDrainLimit);
+    if (lane == 0) s_units[warp >> 1] = units;
+    if (named_bar_or(2, kTcThreads, !ok) && warp == 0) {
+      // of the last tiles' loads those that were not started arrive without one, so that each
+      // tile's barrier completes when what was started has landed
+      uint32_t end = 2 * s_units[1];                     // loads in their order: warps 0, 2, 0, ..
+      if (s_units[0] > 0) end = max(end, 2 * s_units[0] - 1);
+      const uint32_t tiles = (end + KK - 1) / KK, n = (uint32_t)pl.ntile;
+      for (uint32_t i = tiles > n ? tiles - n : 0; i < tiles; ++i) {
+        for (uint32_t u = i * KK; u < (i + 1) * KK; ++u)
+          if (u / 2 >= s_units[u & 1] && lane == 0) mbar_arrive(&bar.full[i % n]);
+        __syncwarp();
+        mbar_wait(&bar.full[i % n], (i / n) & 1, kDrainLimit);
+      }
     }
   } else if (warp == 3) {
     // ------------------------------------------------------------- Q by TMA
@@ -223,7 +235,7 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
     LatentPiece p;
     uint32_t qi = 0, quse = 0;
     while (ok && walk.next(sh, seq_lens, cu_seqlens, nr, KT, kLead, &p)) {
-      if (quse > 0) ok = __all_sync(kAll, mbar_wait(&bar.q_empty[qi], (quse - 1) & 1, kWaitLimit));
+      if (quse > 0) ok = __all_sync(kAll, mbar_wait(&bar.q_empty[qi], (quse - 1) & 1, limit));
       if (!ok) break;
       if (elect_one()) {
         mbar_arrive_expect_tx(&bar.q_full[qi], pl.q_bytes);
@@ -235,7 +247,8 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
         ++quse;
       }
     }
-    for (uint32_t i = 0; !ok && i < (uint32_t)pl.nq; ++i) {
+    const bool bad = named_bar_or(2, kTcThreads, !ok);
+    for (uint32_t i = 0; bad && i < (uint32_t)pl.nq; ++i) {
       const uint32_t uses = quse + (i < qi ? 1 : 0);
       if (uses) mbar_wait(&bar.q_full[i], (uses - 1) & 1, kDrainLimit);
     }
@@ -253,11 +266,11 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
     uint32_t qi = 0, quse = 0;
     while (ok && walk.next(sh, seq_lens, cu_seqlens, nr, KT, kLead, &p)) {
       const uint64_t q0 = dq + (uint64_t)(qi * (pl.q_bytes / 16));
-      ok = __all_sync(kAll, mbar_wait(&bar.q_full[qi], quse & 1, kWaitLimit));
+      ok = __all_sync(kAll, mbar_wait(&bar.q_full[qi], quse & 1, limit));
       for (int i = p.t0; i < p.t1 && ok; ++i, ++t) {
         const uint32_t sb = t % kSBuf;
-        bool go = mbar_wait(&bar.full[slot], use & 1, kWaitLimit);
-        if (t >= kSBuf) go = go && mbar_wait(&bar.s_empty[sb], (t / kSBuf - 1) & 1, kWaitLimit);
+        bool go = mbar_wait(&bar.full[slot], use & 1, limit);
+        if (t >= kSBuf) go = go && mbar_wait(&bar.s_empty[sb], (t / kSBuf - 1) & 1, limit);
         ok = __all_sync(kAll, go);
         if (!ok) break;
         tc_fence_after();
@@ -284,10 +297,10 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
         ++quse;
       }
     }
-    if (!ok) {
+    if (named_bar_or(2, kTcThreads, !ok)) {
       if (elect_one()) mma_commit(&bar.drain[0]);
       __syncwarp();
-      mbar_wait(&bar.drain[0], 0, kWaitLimit);
+      mbar_wait(&bar.drain[0], 0, kDrainLimit);
     }
   } else if (warp == 12) {
     // ------------------------------------------------------------- the values' MMAs
@@ -302,9 +315,9 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
     uint32_t pb = 0, puse = 0;
     while (ok && walk.next(sh, seq_lens, cu_seqlens, nr, KT, kLead, &p)) {
       for (int i = p.t0; i < p.t1; ++i) {
-        bool go = mbar_wait(&bar.p_full[pb], puse & 1, kWaitLimit);
+        bool go = mbar_wait(&bar.p_full[pb], puse & 1, limit);
         if (i == p.t0 && it > 0)                         // the block before has left O^T
-          go = go && mbar_wait(&bar.o_empty, (it - 1) & 1, kWaitLimit);
+          go = go && mbar_wait(&bar.o_empty, (it - 1) & 1, limit);
         ok = __all_sync(kAll, go);
         if (!ok) break;
         tc_fence_after();
@@ -329,10 +342,10 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
       }
       ++it;
     }
-    if (!ok) {
+    if (named_bar_or(2, kTcThreads, !ok)) {
       if (elect_one()) mma_commit(&bar.drain[1]);
       __syncwarp();
-      mbar_wait(&bar.drain[1], 0, kWaitLimit);
+      mbar_wait(&bar.drain[1], 0, kDrainLimit);
     }
   } else {
     // ------------------------------------------------------------- softmax and results
@@ -350,7 +363,7 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
     // PV of the tile `back` tiles ago is done
     auto pv_wait = [&](uint32_t back) {
       const uint32_t t = g - back;
-      return mbar_wait(&bar.pv_done[pl.np == 2 ? t & 1 : 0], (pl.np == 2 ? t >> 1 : t) & 1, kWaitLimit);
+      return mbar_wait(&bar.pv_done[pl.np == 2 ? t & 1 : 0], (pl.np == 2 ? t >> 1 : t) & 1, limit);
     };
     while (!dead && walk.next(sh, seq_lens, cu_seqlens, nr, KT, kLead, &p)) {
       const int low = p.start + p.row_in_seq / sh.H + 1; // the first row's limit, the least
@@ -368,7 +381,7 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
       }
       for (int t = p.t0; t < p.t1; ++t, ++g) {
         const uint32_t sb = kSBuf == 2 ? g & 1 : 0;
-        ok = ok && mbar_wait(&bar.s_full[sb], (kSBuf == 2 ? g >> 1 : g) & 1, kWaitLimit);
+        ok = ok && mbar_wait(&bar.s_full[sb], (kSBuf == 2 ? g >> 1 : g) & 1, limit);
         tc_fence_after();
         const bool mixed = (t + 1) * KT > low;
         uint32_t s[kG][4];
@@ -589,6 +602,7 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
       named_bar(1, kSoft);                               // the block's rows are done with
       if (lane == 0) mbar_arrive(&bar.o_empty);
     }
+    named_bar_or(2, kTcThreads, !ok);
   }
   if (!ok) atomicExch(&g_latent_timeout, 1);
   __syncwarp();
@@ -601,7 +615,8 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
 }
 
 using TcKernel = void (*)(CUtensorMap, CUtensorMap, const int32_t*, const int32_t*,
-                          const int32_t*, bf16*, float*, LatentAttnShape, TcPlan, LatentPartials);
+                          const int32_t*, bf16*, float*, LatentAttnShape, TcPlan, LatentPartials,
+                          uint32_t);
 TcKernel tc_kernel(int nr) {
   switch (nr) {
     case 16: return kda_latent_tc_kernel<16>;
@@ -647,7 +662,7 @@ size_t latent_tc_scratch_bytes(int N, int L, int T, int H, int rank, int sms) {
 cudaError_t launch_latent_tc(const void* q, const void* cache, const int32_t* page_table,
                              const int32_t* seq_lens, const int32_t* cu_seqlens, void* out,
                              float* lse, const LatentAttnShape& sh, int sms, void* buf,
-                             cudaStream_t stream) {
+                             cudaStream_t stream, uint32_t polls) {
   if (!once_per_device(kOnceLatentTc, []() {
         for (int nr = 16; nr <= kTcMaxRows; nr += 16)
           if (cudaFuncSetAttribute(tc_kernel(nr), cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -670,7 +685,7 @@ cudaError_t launch_latent_tc(const void* q, const void* cache, const int32_t* pa
   KDA_TIMED(KDA_KERNEL_LATENT_ATTN, stream,
             tc_kernel(nr)<<<G, kTcThreads, tc_smem(nr), stream>>>(
                 q_map, c_map, page_table, seq_lens, cu_seqlens, static_cast<bf16*>(out), lse, sh,
-                pl, pt));
+                pl, pt, polls));
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   note_launches(1);

@@ -578,6 +578,20 @@ KDA_API int kda_device_status(int reset);
  */
 KDA_API int kda_selftest_bounded_wait(unsigned polls, void* stream);
 
+/*
+ * kda_selftest_latent_waits -- kda_latent_attn (KDA_BF16, page_size a multiple of 8) with each
+ * wait of its tensor-core kernel limited to `polls` polls (0 .. 2^20; 0: every wait gives up at
+ * once), to exercise the same path in a kernel whose roles wait for one another: what is in
+ * flight is waited for, the flag raised, the device stays usable.  Returns KDA_OK,
+ * KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED or KDA_ERR_CUDA.
+ */
+KDA_API int kda_selftest_latent_waits(unsigned polls, const void* q, const void* kv_cache,
+                                      const int32_t* page_table, const int32_t* seq_lens,
+                                      const int32_t* cu_seqlens, void* out, float* lse, int N,
+                                      int L, int H, int rank, int rope, int num_pages,
+                                      int page_size, int max_pages, long long page_stride,
+                                      long long row_stride, float scale, void* stream);
+
 /* Human-readable name of a status code (static storage, never NULL). */
 KDA_API const char* kda_status_string(int status);
 

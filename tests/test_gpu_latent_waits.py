@@ -1,0 +1,54 @@
+"""The latent attention's tensor-core kernel when its waits give up: its roles load, multiply and
+wait for one another, and whichever stops first, what the others have in flight is waited for, the
+flag is raised, and the next call is right.  (No wait is left out and no address is bad: a wait
+that gives up leaves its role, which reads and writes nothing from then on.)"""
+import pytest
+import torch
+
+import gated_delta_rule_74_b200 as kda
+from test_gpu_latent import call, close, make
+
+pytestmark = pytest.mark.gpu
+
+# blocks of 16 to 96 rows, whole blocks and shared ones, few and many tiles
+CASES = {"one": ([40], 1, 12, 512, 64), "ragged": ([3000, 40, 0, 700] * 25, 1, 12, 512, 64),
+         "split": ([20000], 1, 24, 512, 64), "drafts": ([700, 33, 900] * 30, 4, 12, 512, 16),
+         "heads80": ([2000] * 20, 1, 80, 256, 64), "heads96": ([3000, 200] * 20, 1, 96, 512, 64),
+         "chunk": ([4000, 1500], 300, 12, 128, 64)}
+
+
+def limited(x, polls, out, lse):
+    c = lambda t: t.cuda()
+    q, cache, table, lens = c(x["q"]), c(x["cache"]), c(x["table"]), c(x["lens"])
+    N, L, H, D = q.shape
+    rc = kda.lib().kda_selftest_latent_waits(
+        polls, q.data_ptr(), cache.data_ptr(), table.data_ptr(), lens.data_ptr(), None, out.data_ptr(),
+        lse.data_ptr(), N, L, H, x["rank"], D - x["rank"], cache.shape[0], cache.shape[1], table.shape[1],
+        cache.stride(0), cache.stride(1), x["scale"], torch.cuda.current_stream().cuda_stream)
+    assert rc == kda.KDA_OK
+    torch.cuda.synchronize()
+
+
+def outputs(x):
+    B, L, H, _ = x["q"].shape
+    return (torch.full((B, L, H, x["rank"]), 7.0, dtype=torch.bfloat16, device="cuda"),
+            torch.full((B, L, H), 7.0, device="cuda"))
+
+
+@pytest.mark.parametrize("name", CASES)
+def test_waits_that_give_up_are_reported_and_leave_the_device_usable(name):
+    lens, L, H, rank, page = CASES[name]
+    x = make("bf16", lens, L, H, rank, 64, page, seed=3)
+    want = call(x)
+    assert kda.kda_device_status(reset=True) == kda.KDA_OK
+    for polls in (0, 1, 2, 3, 5, 8, 1 << 20):
+        out, lse = outputs(x)
+        limited(x, polls, out, lse)
+        status = kda.kda_device_status(reset=True)
+        assert polls > 0 or status == kda.KDA_ERR_TIMEOUT
+        if polls == 1 << 20 or status == kda.KDA_OK:
+            assert status == kda.KDA_OK
+            assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+        again = call(x)
+        assert kda.kda_device_status(reset=False) == kda.KDA_OK
+        assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
