@@ -23,7 +23,8 @@
 // values'; warps 4..11 do the softmax (two warps a lane quarter of 16 tokens, half of the rows
 // each; a thread holds two tokens and two of every eight rows), the rare rescaling of O^T and the
 // results (thread = value column).  When a wait of one of them gives up, all of them meet at a
-// barrier, and those with loads or MMAs in flight wait for these before the CTA leaves.
+// barrier, and those with loads or MMAs in flight wait for these before the CTA leaves; rows that
+// it had still to finish become NaN.
 // The maximum that the weights refer to moves only when a score passes it by 2^8: a tile then
 // needs one vote, no reduction over the tokens, O^T is rescaled a few times a sequence, and
 // the weights stay below 2^8, far inside of bf16 and fp32.  Sums are kept by thread and
@@ -536,7 +537,7 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
       named_bar(1, kSoft);
       if (wq >= 2 && act) sums(true);
       ok = ok && pv_wait(1);
-      if (named_bar_or(1, kSoft, !ok)) break;
+      if (named_bar_or(1, kSoft, !ok)) { dead = true; break; }
       if (ts < nr) {
         const float z = s_red[ts] + s_red[nr + ts];
         s_row[ts] = z == 0.f ? 0.f : 1.0f / z;
@@ -601,6 +602,23 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
       tc_fence_before();
       named_bar(1, kSoft);                               // the block's rows are done with
       if (lane == 0) mbar_arrive(&bar.o_empty);
+    }
+    // what is left undone when a wait has given up is NaN, not what the memory held before
+    if (dead) {
+      const float bad = __uint_as_float(0x7fffffffu);
+      do {
+        const bool first = p.t0 == 0;
+        if (first && p.t1 == p.tiles) {
+          if (lse && ts < p.rows) lse[p.row0 + ts] = bad;
+          for (int i = ts; i < p.rows * sh.rank; i += kSoft)
+            out[p.row0 * sh.rank + i] = __float2bfloat16_rn(bad);
+        } else {                                           // by the join's weight of it
+          if (ts < nr) pt.lse[(2 * (int)blockIdx.x + (first ? 1 : 0)) * nr + ts] = bad;
+          if (first && ts == 0)
+            pt.head[blockIdx.x] =
+                make_int4((int)p.row0, p.rows, latent_cta_of(p.end, st.W, st.G), 0);
+        }
+      } while (walk.next(sh, seq_lens, cu_seqlens, nr, KT, kLead, &p));
     }
     named_bar_or(2, kTcThreads, !ok);
   }

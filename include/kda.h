@@ -561,7 +561,8 @@ KDA_API int kda_verify_tokens(const float* target, const float* draft,
  * Every wait of the library's kernels on an asynchronous copy or a tensor-core
  * operation polls a bounded number of times.  If a limit runs out (a completion
  * that never arrives), the kernel stops waiting -- its results are then invalid --
- * raises a device flag and finishes, so the GPU never hangs on the library.  This
+ * raises a device flag and finishes, so the GPU never hangs on the library (rows that
+ * kda_latent_attn could not finish are then NaN in out and lse).  This
  * call synchronizes the current device (cudaDeviceSynchronize), reads the flags and,
  * with reset != 0, clears them.  Returns KDA_OK (no wait gave up since the library
  * was loaded or since the last reset), KDA_ERR_TIMEOUT (at least one did) or
