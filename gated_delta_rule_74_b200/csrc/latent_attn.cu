@@ -14,7 +14,8 @@
 // partial sums meet in shared memory.  Output: a thread holds eight rows by four columns in
 // registers (three 16-byte reads for 32 FMAs); with a rank below 512 the threads that
 // remain take other tokens of the tile, and the sums meet at the end of a block.  Bound by
-// these reads, not by the cache's bytes: fp32 has no tensor-core form of fp32 accuracy.
+// these reads, not by the cache's bytes.  (A form on the tensor cores would have to split each
+// operand in three bf16 or TF32 terms to keep fp32's accuracy; it has not been built.)
 // Where there are more rows and shared memory holds but one such CTA an SM, a CTA holds 32 rows
 // and tiles of 16 tokens instead: half a warp a sixteenth of the columns, eight rows by four
 // tokens a thread (12 reads for 128 FMAs), 16 rows by four columns of the output (five for 64).

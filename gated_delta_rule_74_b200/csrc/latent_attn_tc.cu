@@ -33,9 +33,15 @@
 // what the tensor core cuts off at each of 2^18 additions shows).
 // Scores and values are issued by two warps, each of which waits for its own operands alone: one
 // warp for both puts the scores of tile t + 1 before the values of tile t, whose slot then comes
-// free 1100 cycles later (chunk 563 us against 500, 256 sequences 216 against 209, 43 of 96 heads
-// 153 against 145).  The values' products run over 16 tokens at a time and hand those back to
-// the producers at once.
+// free 1100 cycles later (when the second warp came, on the device: 1024-token chunk 563 -> 500 us,
+// 256 sequences 216 -> 209, 43 of 96 heads 153 -> 145; now 521, 203 and 143, after tiles of 48
+// tokens and the results' loop, which cost the chunk 7 us, and the meeting of the roles, which cost
+// it 5).  The values' products run over 16 tokens at a time and hand those back to the producers
+// at once.
+// The weights are rounded to bf16 because both operands of an MMA are of one type, the cached rows'.
+// The sum that divides adds them unrounded: it is the log-sum's too, which stays good to fp32 that
+// way.  A second sum, of the rounded ones, brought the output's error from 0.0020-0.0021 of its norm to
+// 0.0019-0.0020 (its own rounding is 0.0017 of that) and cost 96 heads 4.5% and the chunk 1.5%.
 //
 // Rows of the tile that some query row does not see (the causal edge, what lies behind the
 // length in the last page) have weights of exactly zero; their infinities and NaN would
@@ -64,9 +70,9 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kNone = -3e38f;                    // maximum of a row that has seen nothing
 
 // Tokens of a tile.  64 fill the MMAs' M side, but there is room for more tiles of 48 beside Q at
-// rank 512: three instead of two up to 48 rows (256 sequences of 12 heads 203 us against 209, 100 of
-// 24 heads 96 against 98), two instead of one at 80 and 96 (60 of 80 heads 103 against 128).  Of
-// either two fit at 64 rows.  Tiles of 32 at 16 rows cost more MMAs than they save (242 us).
+// rank 512: three instead of two up to 48 rows (on the device 256 sequences of 12 heads 203 us against
+// 207, 100 of 24 heads 96 against 98), two instead of one at 80 and 96 (60 of 80 heads 104 against
+// 133).  Of either two fit at 64 rows.  Tiles of 32 at 16 rows cost more MMAs than they save (242 us).
 __host__ __device__ constexpr int tc_tile(int nr) { return nr == 64 ? 64 : 48; }
 // Dynamic shared memory: all but 3 KB of the 227 (2 KB at 96 rows) for the variables.
 __host__ __device__ constexpr uint32_t tc_smem(int nr) { return nr > 80 ? 230400 : 229376; }
@@ -129,7 +135,8 @@ kda_latent_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                      float* __restrict__ lse, LatentAttnShape sh, TcPlan pl, LatentPartials pt,
                      uint32_t limit) {
   constexpr int nr = NR, KT = tc_tile(NR), KK = KT / 16, kSBuf = NR <= 80 ? 2 : 1;
-  // tiles that a block costs besides its own (193 sequences of 3 blocks: 124 us, 133 with 2 and 3)
+  // tiles that a block costs besides its own (193 sequences of 3 blocks, rank 384: 122 us, 127 with 2
+  // and 3; rank 128 92 and 96; rank 512 with position values 173 and 169)
   constexpr int kLead = NR <= 48 ? 3 : 5;
   constexpr uint32_t kTmemS = 4 * NR;
   // the alignment is part of the declaration: there is no room to round up
@@ -648,11 +655,12 @@ TcKernel tc_kernel(int nr) {
 
 // Rows of a block: all of a sequence's up to 64, a multiple of 16.  Up to 96: all of them, or, of
 // few sequences, two blocks of 48: the CTAs then share a sequence by many, and what they
-// write and join counts for more than reading the cache twice (96 heads, 4000 to 8192 tokens: 4
-// sequences 34 us against 42, 16 58 against 65, 24 79 either way; 43 of up to 16384 160 against
-// 146).  Of more rows, 64, whose tiles of 64 tokens cost the MMAs less a row and token than
-// 96 or 48 with tiles of 48 (a 1024-token chunk of 12 heads behind 8192 to 32768 tokens: 507 us
-// against 541 and 539).
+// write and join counts for more than reading the cache twice (on the device, 96 heads, 4000 to 8192
+// tokens: 4 sequences 35 us against 42, 16 58 against 63, 24 78 against 77; 43 of up to 16384 160
+// against 143; of 400 tokens 4 sequences 21 against 25, 16 23 against 27, of 50 19 against 23 and 21
+// against 25).  Of more rows, 64, whose tiles of 64 tokens cost the MMAs less a row and token than
+// 96 or 48 with tiles of 48 (a 1024-token chunk of 12 heads behind 8192 to 32768 tokens: 521 us
+// against 537 and 573).
 // Packed, a sequence has so many on average, which says little when one has most of them: from 1024
 // rows on that are more than a token for each sequence, at least 48 (512 slots, all empty but for
 // a 1024-token chunk of 12 heads behind 16384: 32 rows 804 us, 48 594, 64 553; 256 sequences of two
