@@ -304,12 +304,14 @@ __device__ __forceinline__ void join_add(float4& a, float w, const float4& v) {
 }
 
 // Many items: block (c, y) takes rows y, y + gridDim.y, .. (or fours of rows) of the shared block
-// that starts in CTA c, if one does.  Few (`list`): the blocks that there are get listed and
-// their rows spread over the grid.
+// that starts in CTA c, if one does.  Few (kList): the blocks that there are get listed and
+// their rows spread over the grid.  kEither: so, if a block of many CTAs has rows for more than two
+// rounds of its y.
+enum { kEach = 0, kList = 1, kEither = 2 };
 template <typename T>
 __global__ void __launch_bounds__(kJT)
 kda_latent_join_kernel(T* __restrict__ out, float* __restrict__ lse, LatentPartials pt, int G,
-                       int nr, int rank, bool list) {
+                       int nr, int rank, int form) {
   __shared__ float s_w[kLatentMaxCtas];
   __shared__ float4 s_part[kJT / 32][32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -317,7 +319,17 @@ kda_latent_join_kernel(T* __restrict__ out, float* __restrict__ lse, LatentParti
   __shared__ int s_list[kLatentMaxCtas], s_n;
   __shared__ uint32_t s_mask[kLatentMaxCtas / 32];
   int c0 = blockIdx.x;
+  const int parts = rank / 128;                        // units of a row
   sm100::grid_dep_wait();
+  bool list = form == kList;
+  if (form == kEither) {
+    bool far = false;
+    for (int c = tid; c < G; c += kJT) {
+      const int4 h = pt.head[c];
+      far = far || (h.z - c >= kSome && h.y * parts > 2 * (int)gridDim.y);
+    }
+    list = __syncthreads_or(far);
+  }
   if (list) {                                          // in the CTAs' order: every block's is the same
     for (int c = tid; c - lane < G; c += kJT) {
       const uint32_t some = __ballot_sync(0xffffffffu, c < G && pt.head[c].y > 0);
@@ -366,7 +378,6 @@ kda_latent_join_kernel(T* __restrict__ out, float* __restrict__ lse, LatentParti
     }
     return;
   }
-  const int parts = rank / 128;                        // units of a row
   if (!list && k <= kSome) {
     constexpr int kWarps = kJT / 32;
     for (int u = blockIdx.y * kWarps + warp; u < hd.y * parts; u += gridDim.y * kWarps) {
@@ -397,7 +408,8 @@ kda_latent_join_kernel(T* __restrict__ out, float* __restrict__ lse, LatentParti
     }
     return;
   }
-  const int u0 = list ? blockIdx.x : blockIdx.y, du = list ? gridDim.x : gridDim.y;
+  const int u0 = list ? blockIdx.y * gridDim.x + blockIdx.x : blockIdx.y;
+  const int du = list ? gridDim.x * gridDim.y : gridDim.y;
   const int units = (list ? s_n * nr : hd.y) * parts;
   for (int u = u0; u < units; u += du) {
     int r = u / parts;
@@ -504,42 +516,43 @@ cudaError_t run_simt(const void* q, const void* cache, const int32_t* page_table
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   note_launches(1);
-  return launch_latent_join(out, lse, pt, G, rows, sh.rank, latent_items(sh, rows),
-                            sizeof(T) == 2 ? KDA_BF16 : KDA_F32, stream);
+  return launch_latent_join(out, lse, pt, G, rows, sh, sizeof(T) == 2 ? KDA_BF16 : KDA_F32, stream);
 }
 
 }  // namespace
 
-// `items`: blocks of rows of the call (packed: at most).  Few of them, each over more than 16
-// CTAs, are listed and spread over the grid, two rounds at most of 2 us (8 sequences of 16 heads,
-// rank 128: 15.7 us a call against 17.7; a list of many is slow: 100 sequences of one head behind
-// 500 tokens 55 us against 22); a warp for each 128 columns of a row where some
-// CTAs share it (16 sequences of 12 heads: 27.0 against 30.8 listed); else blocks of 8 rows, of
-// which many find nothing to do.
+// Few blocks of rows, each over more than 16 CTAs, are listed and spread over the grid, two rounds at
+// most of 2 us (8 sequences of 16 heads, rank 128: 15.7 us a call against 17.7); a warp for each 128
+// columns of a row where some CTAs share it (16 sequences of 12 heads: 27.0 against 30.8 listed); else
+// blocks of 8 rows, of which many find nothing to do.  A packed call's blocks are as many as its rows
+// fill, or as its sequences with tokens.  Where one count is few and the other not, the kernel looks
+// (on the device, by the first count alone 100 sequences of one head behind 500 tokens took 53 us,
+// by the second 22, so 23; two of eight tokens behind 30000 among 62 empty slots 23, 57 and 24).
 cudaError_t launch_latent_join(void* out, float* lse, const LatentPartials& pt, int G, int nr,
-                               int rank, long long items, int dtype, cudaStream_t stream) {
-  const int units = nr * (rank / 128);
-  const bool list = items * units <= 8LL * G && items * 16 < G;
-  const int y = items * kFew <= 2LL * G ? (units + 15) / 16 : nr <= 32 ? 4 : (nr + 7) / 8;
-  const long long most = 4LL * G, work = items * units;
-  const dim3 grid = list ? dim3((unsigned)(work < most ? work : most)) : dim3(G, y);
+                               const LatentAttnShape& sh, int dtype, cudaStream_t stream) {
+  const int rank = sh.rank, units = nr * (rank / 128);
+  const bool packed = sh.L == 0;
+  const long long tokens = packed ? sh.T : sh.L;             // uniform: of a sequence
+  const long long full = (tokens * sh.H + nr - 1) / nr, each = tokens * ((sh.H + nr - 1) / nr);
+  const long long items = packed ? full : sh.N * full;       // packed: at least
+  const long long own = tokens * sh.H / nr + (sh.N < tokens ? sh.N : tokens);
+  const long long at_most = !packed ? items : own < each ? own : each;
+  const long long work = packed ? tokens * sh.H * (rank / 128) : items * units, most = 4LL * G;
+  auto few = [&](long long n) { return work <= 8LL * G && n * 16 < G; };
+  const int form = !few(items) ? kEach : few(at_most) ? kList : kEither;
+  const int y = at_most * kFew <= 2LL * G ? (units + 15) / 16 : nr <= 32 ? 4 : (nr + 7) / 8;
+  const dim3 grid = form == kList ? dim3((unsigned)(at_most * units < most ? at_most * units : most)) : dim3(G, y);
   cudaError_t e = cudaSuccess;
   if (dtype == KDA_BF16)
     KDA_TIMED(KDA_KERNEL_LATENT_ATTN, stream,
               e = launch_after(kda_latent_join_kernel<__nv_bfloat16>, grid, dim3(kJT), 0, stream,
-                               static_cast<__nv_bfloat16*>(out), lse, pt, G, nr, rank, list));
+                               static_cast<__nv_bfloat16*>(out), lse, pt, G, nr, rank, form));
   else
     KDA_TIMED(KDA_KERNEL_LATENT_ATTN, stream,
               e = launch_after(kda_latent_join_kernel<float>, grid, dim3(kJT), 0, stream,
-                               static_cast<float*>(out), lse, pt, G, nr, rank, list));
+                               static_cast<float*>(out), lse, pt, G, nr, rank, form));
   note_launches(1);
   return e;
-}
-
-long long latent_items(const LatentAttnShape& sh, int nr) {
-  // packed: the whole blocks that there can be, and one more for each sequence with tokens
-  return sh.L > 0 ? sh.N * (((long long)sh.L * sh.H + nr - 1) / nr)
-                  : (long long)sh.T * sh.H / nr + (sh.N < sh.T ? sh.N : sh.T);
 }
 
 size_t latent_attn_scratch_bytes(int N, int L, int T, int H, int rank, int rope, int page_size,

@@ -64,9 +64,7 @@ cudaError_t launch_latent_tc(const void* q, const void* cache, const int32_t* pa
                              float* lse, const LatentAttnShape& sh, int sms, void* buf,
                              cudaStream_t stream, uint32_t polls);
 cudaError_t launch_latent_join(void* out, float* lse, const LatentPartials& pt, int G, int nr,
-                               int rank, long long items, int dtype, cudaStream_t stream);
-// Blocks of nr rows of a call (packed: at most).
-long long latent_items(const LatentAttnShape& sh, int nr);
+                               const LatentAttnShape& sh, int dtype, cudaStream_t stream);
 
 // ------------------------------------------------------------------ device side
 // sum_{i < n} floor((a i + b) / m), a, b >= 0, m > 0

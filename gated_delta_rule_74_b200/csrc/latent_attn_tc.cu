@@ -715,7 +715,7 @@ cudaError_t launch_latent_tc(const void* q, const void* cache, const int32_t* pa
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   note_launches(1);
-  return launch_latent_join(out, lse, pt, G, nr, sh.rank, latent_items(sh, nr), KDA_BF16, stream);
+  return launch_latent_join(out, lse, pt, G, nr, sh, KDA_BF16, stream);
 }
 
 // Reads (and with reset clears) g_latent_timeout; host side of kda_device_status.

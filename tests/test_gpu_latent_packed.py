@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import gated_delta_rule_74_b200 as kda
+from latent_sharp import counting, counts_right
 from test_gpu_latent import call, close, make
 
 pytestmark = pytest.mark.gpu
@@ -65,3 +66,21 @@ def test_one_long_chunk_among_empty_and_one_token_sequences(dtype, H):
         lens[at] = 450
         x = make(dtype, lens, cu[-1], H, 128, 64, 64, cu=cu, seed=at + others)
         close(x, *call(x))
+
+
+@pytest.mark.parametrize("slots,new,ctx,H", [(64, [8, 8], 30000, 2), (128, [17], 60000, 1), (128, [5], 30000, 12)])
+def test_few_sequences_among_empty_slots(slots, new, ctx, H):
+    """Empty slots add nothing to the time of the few sequences whose blocks many CTAs share (by half
+    at most; counted as if each token could be a sequence's only one, the first took 57 us for 23)."""
+    times = []
+    for empty in (0, slots - len(new)):
+        k = new + [0] * empty
+        cu = [0]
+        for n in k:
+            cu.append(cu[-1] + n)
+        x = counting(make("bf16", [ctx if n else 0 for n in k], cu[-1], H, 512, 64, 64, cu=cu))
+        counts_right(x, *call(x))
+        d = {k: (v.cuda() if isinstance(v, torch.Tensor) else v) for k, v in x.items()}
+        times.append(device_us(lambda: kda.kda_latent_attn(
+            d["q"], d["cache"], d["table"], d["lens"], rank=512, scale=x["scale"], cu_seqlens=d["cu"])))
+    assert times[1] <= 1.5 * times[0], times
