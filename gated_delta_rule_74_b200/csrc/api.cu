@@ -18,7 +18,7 @@ void note_launches(unsigned long long n) { g_launches.fetch_add(n, std::memory_o
 namespace {
 
 constexpr int kVersionMajor = 0;
-constexpr int kVersionMinor = 2;
+constexpr int kVersionMinor = 3;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool head_ok(int d) { return d == 64 || d == 128; }
